@@ -90,6 +90,38 @@ int moe_router_gemm(int dtype, const void* x, const void* w_r, int T, int d, int
 int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float* topk_w,
               hipStream_t stream);
 
+/* ----------------------------------------------------------------- norm
+ * moe_add_rmsnorm: what a block runs on its token rows before the layer.
+ *   h[t] = x[t] + res[t], rounded to `dtype`     (res given)
+ *   rs   = 1 / sqrt(mean_i(h[t,i]^2) + eps)      (of h as it is stored; binary32)
+ *   y[t,i] = h[t,i] * rs * w[i], rounded once to `dtype`
+ * With res NULL, h is x itself and must be NULL here. The MXFP8 copy (q, s),
+ * bf16 with d % 128 == 0 only, holds the rows of y exactly as moe_mx_quantize
+ * axis 0 writes them from the rounded y: codes q [T,d], scales s of T*d/32
+ * bytes; both or neither NULL. y may be NULL when the copy is given. rstd [T]
+ * binary32 (may be NULL) receives rs for the backward pass.
+ *   x, res, h, y [T,d] and w [d] of `dtype`; d <= MOE_MAX_NORM_D; eps > 0.
+ * h may be res or x itself and y may be x itself; other overlaps are not
+ * allowed. Values whose squares overflow binary32 give rs = 0.
+ *
+ * moe_add_rmsnorm_bwd: derived, its adjoint, with n = h * rs and g = dy * w:
+ *   dx[t] = dh[t] + rs * (g - n * mean_i(g * n)), rounded once to `dtype`:
+ *           the gradient of x and of res alike; dh (may be NULL) is what
+ *           arrives at h along the residual
+ *   dw    = sum_t dy[t] * n[t], binary32 sums in a fixed order, rounded once
+ *           to `dtype`; dw may be NULL (a frozen w): then ws may be NULL too
+ *   dy, h, dh, dx [T,d], w and dw [d] of `dtype`; rstd [T] from the forward;
+ *   ws of at least moe_add_rmsnorm_bwd_workspace_bytes(T, d) bytes, 16-byte
+ *   aligned. dx may be dy or dh itself. With T == 0 dw is zero. Calls sharing
+ *   one workspace must be ordered on one stream. */
+#define MOE_MAX_NORM_D 12288
+int moe_add_rmsnorm(int dtype, const void* x, const void* res, const void* w, int T, int d, float eps,
+                    void* h, void* y, void* q, void* s, float* rstd, hipStream_t stream);
+size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int d);
+int moe_add_rmsnorm_bwd(int dtype, const void* dy, const void* h, const void* w, const float* rstd,
+                        const void* dh, int T, int d, void* dx, void* dw, void* ws, size_t ws_bytes,
+                        hipStream_t stream);
+
 /* ----------------------------------------------------------------- metadata
  * moe_offsets: GPU-resident routing metadata (deniz.in, "Yeni stack nasıl
  * çalışıyor": split and group sizes never leave the GPU).
@@ -357,6 +389,21 @@ int moe_mx_quantize(const void* src, int rows, int cols, int axis, const int32_t
 int moe_permute_mx(const void* x, int T, int d, int k, const int32_t* src_slot,
                    const int32_t* group_offsets, int E, int n_rows, int col_stride, void* q_rows,
                    void* s_rows, void* q_cols, void* s_cols, hipStream_t stream);
+
+/* moe_mx_dequantize: the values of rows quantised along axis 0 (codes q
+ * [rows, cols], scales s in the layout of moe_mx_quantize), as bf16 dst
+ * [rows, cols]; cols % 128 == 0. Exact, except that products below bf16's
+ * subnormal range round to it. A scale code 0xFF is not a value.
+ *
+ * moe_permute_from_mx: moe_permute of token rows that are held as their MXFP8
+ * copy (the input of a layer kept in 8 bits between its passes):
+ * x_perm[row_of[s]] = deq(q[s / k]) for every kept slot s, and x = deq(q)
+ * unless x is NULL, both from one read of the codes. src_slot as for
+ * moe_permute.
+ *   q, s: T rows of d, d % 128 == 0; x [T,d], x_perm [n_rows,d] bf16. */
+int moe_mx_dequantize(const void* q, const void* s, int rows, int cols, void* dst, hipStream_t stream);
+int moe_permute_from_mx(const void* q, const void* s, int T, int d, int k, const int32_t* row_of,
+                        const int32_t* src_slot, int n_rows, void* x, void* x_perm, hipStream_t stream);
 
 /* moe_grouped_gemm_mx: the six expert GEMMs of moe_grouped_gemm with every
  * operand MXFP8 (blocks of 32 along that GEMM's contraction), binary32

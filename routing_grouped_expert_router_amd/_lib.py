@@ -57,6 +57,9 @@ SIGNATURES = {
     "moe_abi_version": (_i, []),
     "moe_router_gemm": (_i, [_i, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "moe_route": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_add_rmsnorm": (_i, [_i, _vp, _vp, _vp, _i, _i, C.c_float, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_add_rmsnorm_bwd_workspace_bytes": (_sz, [_i, _i]),
+    "moe_add_rmsnorm_bwd": (_i, [_i, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "moe_offsets_workspace_bytes": (_sz, [_i, _i, _i]),
     "moe_offsets": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_offsets_noalloc": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -73,6 +76,8 @@ SIGNATURES = {
     "moe_mx_quantize": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp]),
     "moe_mx_quantize_both": (_i, [_vp, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
     "moe_permute_mx": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "moe_mx_dequantize": (_i, [_vp, _vp, _i, _i, _vp, _vp]),
+    "moe_permute_from_mx": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp]),
     "moe_grouped_gemm_mx_workspace_bytes": (_sz, [C.POINTER(moe_mx_gg_desc)]),
     "moe_grouped_gemm_mx": (_i, [C.POINTER(moe_mx_gg_desc), _vp]),
 }
@@ -186,6 +191,19 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _same_device(*tensors):
+    """The launches go to the current device's stream: raise for a device
+    tensor on another one."""
+    cur = None
+    for t in tensors:
+        if t is None or not t.is_cuda:
+            continue
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.device.index != cur:
+            raise MoEError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
 def _fill(desc, fields):
     """Set descriptor pointer fields once every tensor has passed its layout
     check; raise if any of them is in host memory."""
@@ -193,6 +211,13 @@ def _fill(desc, fields):
         raise MoEError("libmoe needs device tensors")
     for obj, name, v in ((o, n, v) for (o, n), v in fields):
         setattr(obj, name, v)
+
+
+class MxTensor:
+    """E4M3 codes and E8M0 scales of one quantised operand (uint8 tensors)."""
+
+    def __init__(self, q: torch.Tensor, s: torch.Tensor):
+        self.q, self.s = q, s
 
 
 def moe_status_string(status: int) -> str:
@@ -215,6 +240,33 @@ def moe_route(logits, k, topk_idx, topk_w, stream=None):
     _call("moe_route", _req(logits, "logits", torch.float32, (T, E)), T, E, k,
                            _req(topk_idx, "topk_idx", torch.int32, (T, k)),
                            _req(topk_w, "topk_w", torch.float32, (T, k)), _stream(stream))
+
+
+# ----------------------------------------------------------------- norm
+def moe_add_rmsnorm(x, w, eps, res=None, h=None, y=None, q: Optional[MxTensor] = None, rstd=None, stream=None):
+    T, d = x.shape
+    dt, u8 = x.dtype, torch.uint8
+    _same_device(x, w, res, h, y, rstd, *((q.q, q.s) if q is not None else ()))
+    _call("moe_add_rmsnorm", _dt(x), _req(x, "x", _FLOATS, (T, d)), _req(res, "res", dt, (T, d), optional=True),
+          _req(w, "w", dt, (d,)), T, d, eps, _req(h, "h", dt, (T, d), optional=True),
+          _req(y, "y", dt, (T, d), optional=True),
+          None if q is None else _req(q.q, "q.q", u8, min_numel=T * d),
+          None if q is None else _req(q.s, "q.s", u8, min_numel=T * d // 32),
+          _req(rstd, "rstd", torch.float32, (T,), optional=True), _stream(stream))
+
+
+def moe_add_rmsnorm_bwd_workspace_bytes(T, d) -> int:
+    return lib().moe_add_rmsnorm_bwd_workspace_bytes(T, d)
+
+
+def moe_add_rmsnorm_bwd(dy, h, w, rstd, dx, dw=None, dh=None, ws=None, stream=None):
+    T, d = dy.shape
+    dt = dy.dtype
+    _same_device(dy, h, w, rstd, dx, dw, dh, ws)
+    _call("moe_add_rmsnorm_bwd", _dt(dy), _req(dy, "dy", _FLOATS, (T, d)), _req(h, "h", dt, (T, d)),
+          _req(w, "w", dt, (d,)), _req(rstd, "rstd", torch.float32, (T,)), _req(dh, "dh", dt, (T, d), optional=True),
+          T, d, _req(dx, "dx", dt, (T, d)), _req(dw, "dw", dt, (d,), optional=True), _p(ws),
+          0 if ws is None else _nbytes(ws), _stream(stream))
 
 
 def moe_offsets_workspace_bytes(T, k, E) -> int:
@@ -349,13 +401,6 @@ def moe_grouped_gemm(desc: moe_gg_desc, stream=None):
 
 
 # ----------------------------------------------------------------- MXFP8
-class MxTensor:
-    """E4M3 codes and E8M0 scales of one quantised operand (uint8 tensors)."""
-
-    def __init__(self, q: torch.Tensor, s: torch.Tensor):
-        self.q, self.s = q, s
-
-
 def moe_mx_col_stride(rows: int, n_groups: int) -> int:
     return lib().moe_mx_col_stride(rows, n_groups)
 
@@ -377,6 +422,25 @@ def moe_mx_quantize_both(src, rows_out: MxTensor, cols_out: MxTensor, group_offs
                                       n_groups, col_stride, _req(rows_out.q, "q_rows", u8), _req(rows_out.s, "s_rows", u8),
                                       _req(cols_out.q, "q_cols", u8), _req(cols_out.s, "s_cols", u8),
                                       _stream(stream))
+
+
+def moe_mx_dequantize(src: MxTensor, dst, stream=None):
+    rows, cols = dst.shape
+    u8 = torch.uint8
+    _same_device(src.q, src.s, dst)
+    _call("moe_mx_dequantize", _req(src.q, "q", u8, min_numel=rows * cols),
+          _req(src.s, "s", u8, min_numel=rows * cols // 32), rows, cols, _req(dst, "dst", torch.bfloat16),
+          _stream(stream))
+
+
+def moe_permute_from_mx(src: MxTensor, k, row_of, src_slot, x_perm, x=None, stream=None):
+    n, d = x_perm.shape
+    T = row_of.numel() // k if k > 0 else 0
+    u8, i32, bf = torch.uint8, torch.int32, torch.bfloat16
+    _same_device(src.q, src.s, row_of, src_slot, x_perm, x)
+    _call("moe_permute_from_mx", _req(src.q, "q", u8, min_numel=T * d), _req(src.s, "s", u8, min_numel=T * d // 32),
+          T, d, k, _req(row_of, "row_of", i32, T * k), _req(src_slot, "src_slot", i32, n, optional=True), n,
+          _req(x, "x", bf, (T, d), optional=True), _req(x_perm, "x_perm", bf, (n, d)), _stream(stream))
 
 
 def moe_permute_mx(x, k, src_slot, group_offsets, E, col_stride, rows_out: MxTensor, cols_out: MxTensor,

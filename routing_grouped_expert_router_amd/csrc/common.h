@@ -77,6 +77,11 @@ MOE_DEV V16 keep_if(bool ok, const V16& v) {
   return o;
 }
 
+// Holds a loaded vector in registers from here on. Without it the compiler
+// may move a load down to each of its conditional uses (a store per routed
+// row, an FMA per valid slot) and reload it there, one wait per use.
+MOE_DEV void pin(V16& v) { asm volatile("" : "+v"(v.w[0]), "+v"(v.w[1]), "+v"(v.w[2]), "+v"(v.w[3])); }
+
 // Elements per 16-byte vector.
 template <typename T> constexpr int kVec = 16 / sizeof(T);
 

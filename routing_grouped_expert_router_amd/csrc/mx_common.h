@@ -102,4 +102,20 @@ MOE_DEV uint32_t quantize_block_bf16(const uint32_t* w, V16 (&out)[2]) {
   return static_cast<uint32_t>(b.x + 127);
 }
 
+// Eight codes under one scale code -> eight bf16 values. The conversion
+// multiplies by 2^X exactly (scale operand as in cvt_scale) and every product
+// of an E4M3 value from 2^-9 up and a scale from 2^-124 up is a bf16 value.
+MOE_DEV V16 decode8(uint2 q, uint32_t code) {
+  const float scale = cvt_scale(static_cast<int>(code) - 127);
+  V16 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? q.x : q.y;
+    const bf16x2 p = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true)
+                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+    v.w[i] = __builtin_bit_cast(uint32_t, p);
+  }
+  return v;
+}
+
 }  // namespace moe

@@ -1,0 +1,378 @@
+// Residual addition with root-mean-square norm, forward and backward (gfx950):
+// what a transformer block runs on the token rows before the expert layer.
+//
+//   h = x + res (rounded to the storage type),  rs = 1 / sqrt(mean(h^2) + eps),
+//   y = h * rs * w,  and optionally the MXFP8 copy of y along each row.
+//   n = h * rs,  g = dy * w:  dx = dh + rs * (g - n * mean(g * n)),  dw = sum_t dy * n
+//
+// Memory-bound in both directions: every element is read and written once, and
+// a whole row stays in the registers of the 1 to 12 waves that share it, so
+// the norm and the quantisation cost no second pass. See include/moe.h for the
+// contract of each entry point.
+#include "mx_common.h"
+
+namespace moe {
+
+namespace {
+
+// 16-byte pieces of a row per lane: W waves hold rows of up to 256 W pieces.
+constexpr int kNormPieces = 4;
+
+// Waves per row: the fewest of 1, 4 and 6 (bf16) or 12 (binary32) that hold
+// the row, up to MOE_MAX_NORM_D (16 waves of one workgroup would leave the
+// backward kernel 128 registers each, fewer than it needs).
+template <typename T> constexpr int kNormMaxWaves = MOE_MAX_NORM_D / (64 * kNormPieces * kVec<T>);
+
+struct NormArgs {
+  const void* x;
+  const void* res;   // null: h = x, not written
+  const void* w;
+  void* h;
+  void* y;           // null: only the MXFP8 copy
+  uint8_t* q;        // null: no MXFP8 copy
+  uint8_t* s;
+  float* rstd;       // null: not wanted
+  int T, d;
+  float eps;
+};
+
+// Piece c of a row: a wave-uniform base and a 32-bit byte offset, so that the
+// address costs one register.
+template <typename T> MOE_DEV V16 load_piece(const T* row, uint32_t c) {
+  return *reinterpret_cast<const V16*>(reinterpret_cast<const char*>(row) + c * 16u);
+}
+template <typename T> MOE_DEV void store_piece(T* row, uint32_t c, const V16& v) {
+  *reinterpret_cast<V16*>(reinterpret_cast<char*>(row) + c * 16u) = v;
+}
+MOE_DEV uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// Sum over the W waves of a row; `red` holds one float per wave of the
+// workgroup and is not reused before another barrier.
+template <int W> MOE_DEV float row_sum(float v, float* red, int wave) {
+  v = wave_sum(v);
+  if constexpr (W == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[wave] = v;
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) t += red[i];
+  return t;
+}
+
+template <int W> constexpr int kNormThreads = W > 4 ? 64 * W : 256;
+
+template <typename T, int W, bool MX>
+__global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a) {
+  constexpr int V = kVec<T>, U = kNormPieces;
+  __shared__ float red[W > 4 ? W : 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const size_t t = W == 1 ? (size_t)blockIdx.x * 4 + wave : blockIdx.x;
+  if (t >= (size_t)a.T) return;   // W == 1 only: no barrier follows there
+  const int d = a.d;
+  const uint32_t nvec = d / V, c0 = (W == 1 ? 0 : wave * 64) + lane;
+  // all loads first, unconditional: a piece past the row reads its last one
+  const T* xp = static_cast<const T*>(a.x) + t * d;
+  const T* rp = static_cast<const T*>(a.res ? a.res : a.x) + t * d;
+  const T* wp = static_cast<const T*>(a.w);
+  V16 hv[U], rv[U], wv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) hv[u] = load_piece(xp, umin(c0 + 64 * W * u, nvec - 1));
+  if (a.res) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) rv[u] = load_piece(rp, umin(c0 + 64 * W * u, nvec - 1));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) wv[u] = load_piece(wp, umin(c0 + 64 * W * u, nvec - 1));
+  float ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool in = c0 + 64 * W * u < nvec;
+    float f[V];
+    unpack(hv[u], f);
+    if (a.res) {
+      float r[V];
+      unpack(rv[u], r);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] += r[i];
+      hv[u] = pack(f);     // the norm is taken of h as it is stored
+      unpack(hv[u], f);
+      if (in) store_piece(static_cast<T*>(a.h) + t * d, c0 + 64 * W * u, hv[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss += in ? f[i] * f[i] : 0.f;
+  }
+  ss = row_sum<W>(ss, red, wave);
+  const float rs = 1.0f / sqrtf(ss / (float)d + a.eps);
+  if (a.rstd && c0 == 0) a.rstd[t] = rs;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t c = c0 + 64 * W * u;
+    float f[V], w[V];
+    unpack(hv[u], f);
+    unpack(wv[u], w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = f[i] * rs * w[i];
+    const V16 yv = pack(f);
+    if (a.y && c < nvec) store_piece(static_cast<T*>(a.y) + t * d, c, yv);
+    if constexpr (MX) {
+      // four lanes hold a block of 32 values, sixteen the four blocks of a
+      // scale word (nvec is a multiple of 16: no group straddles the row's end)
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = mag_max2(m, yv.w[i]);
+      m = max2(m, __shfl_xor(m, 1, 64));
+      m = max2(m, __shfl_xor(m, 2, 64));
+      const BlockScale bs = block_scale(max_half(m));
+      const uint2 o = make_uint2(encode_quad(yv.w[0], yv.w[1], bs), encode_quad(yv.w[2], yv.w[3], bs));
+      const uint32_t code = static_cast<uint32_t>(bs.x + 127);
+      const uint32_t word = code | __shfl_down(code, 4, 64) << 8 | __shfl_down(code, 8, 64) << 16 |
+                            __shfl_down(code, 12, 64) << 24;
+      if (c < nvec) {
+        reinterpret_cast<uint2*>(a.q + t * d)[c] = o;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(a.s + 4 * (static_cast<size_t>(a.T) * (c >> 4) + t)) = word;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ backward
+struct NormBwdArgs {
+  const void* dy;
+  const void* h;
+  const void* w;
+  const float* rstd;
+  const void* dh;    // null: nothing arrives along the residual
+  void* dx;
+  float* part;       // [gridDim.x][d] sums of dy * n over a workgroup's rows; null: dw is not wanted
+  int T, d;
+};
+
+// Workgroups stride over the rows and keep their share of dw in registers.
+template <typename T, int W>
+__global__ void __launch_bounds__(kNormThreads<W>) rmsnorm_bwd_kernel(NormBwdArgs a) {
+  constexpr int V = kVec<T>, U = kNormPieces, RPB = W == 1 ? 4 : 1;
+  __shared__ float red[2][W > 4 ? W : 4];
+  __shared__ float sums[W == 1 ? 64 * U * V : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int d = a.d;
+  const uint32_t nvec = d / V, c0 = (W == 1 ? 0 : wave * 64) + lane;
+  const T* wp = static_cast<const T*>(a.w);
+  V16 wv[U];
+  float dw[U][V];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    wv[u] = load_piece(wp, umin(c0 + 64 * W * u, nvec - 1));
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[u][i] = 0.f;
+  }
+  int par = 0;
+  for (size_t t = (size_t)blockIdx.x * RPB + (W == 1 ? wave : 0); t < (size_t)a.T; t += (size_t)gridDim.x * RPB) {
+    const T* gp = static_cast<const T*>(a.dy) + t * d;
+    const T* hp = static_cast<const T*>(a.h) + t * d;
+    const T* rp = static_cast<const T*>(a.dh ? a.dh : a.dy) + t * d;
+    V16 gv[U], hv[U], rv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      gv[u] = load_piece(gp, umin(c0 + 64 * W * u, nvec - 1));
+      hv[u] = load_piece(hp, umin(c0 + 64 * W * u, nvec - 1));
+    }
+    if (a.dh) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) rv[u] = load_piece(rp, umin(c0 + 64 * W * u, nvec - 1));
+    }
+    const float rs = a.rstd[t];
+    float dot = 0.f;   // sum of g * n
+    // held packed across the phases: unpacked copies would take 150 registers
+#pragma unroll
+    for (int u = 0; u < U; ++u) pin(wv[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = c0 + 64 * W * u < nvec;
+      float g[V], n[V], w[V];
+      unpack(gv[u], g);
+      unpack(hv[u], n);
+      unpack(wv[u], w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float p = in ? g[i] * (n[i] * rs) : 0.f;
+        dw[u][i] += p;
+        dot += p * w[i];
+      }
+    }
+    dot = row_sum<W>(dot, red[par], wave);
+    par ^= 1;          // the next row's sums must not overwrite these before every wave has read them
+    const float mean = dot / (float)d;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      pin(gv[u]);
+      pin(hv[u]);
+      pin(wv[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t c = c0 + 64 * W * u;
+      float g[V], n[V], w[V], r[V];
+      unpack(gv[u], g);
+      unpack(hv[u], n);
+      unpack(wv[u], w);
+      if (a.dh) unpack(rv[u], r);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float v = rs * (g[i] * w[i] - (n[i] * rs) * mean);
+        g[i] = a.dh ? r[i] + v : v;
+      }
+      if (c < nvec) store_piece(static_cast<T*>(a.dx) + t * d, c, pack(g));
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + (size_t)blockIdx.x * d;
+  if constexpr (W == 1) {
+    // the four waves' sums, added in wave order
+    for (int k = 0; k < 4; ++k) {
+      if (wave == k) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float* p = sums + (64 * u + lane) * V + i;
+            *p = k ? *p + dw[u][i] : dw[u][i];
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < d; c += 256) out[c] = sums[c];
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t c = c0 + 64 * W * u;
+      if (c < nvec) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          *reinterpret_cast<float4*>(out + (size_t)c * V + i) = make_float4(dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]);
+      }
+    }
+  }
+}
+
+// dw[c] = sum over the parts, in a fixed order: 64 threads of a workgroup take
+// every 64th part of 4 columns each, then their sums are added in LDS.
+constexpr int kRedCols = 64;
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int parts, int d,
+                                                       T* __restrict__ dw) {
+  __shared__ float4 acc[64][kRedCols / 4];
+  const int ci = threadIdx.x & 15, gi = threadIdx.x >> 4;
+  const int c = blockIdx.x * kRedCols + 4 * ci;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < d) {
+    for (int g = gi; g < parts; g += 64) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)g * d + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+  }
+  acc[gi][ci] = s;
+  __syncthreads();
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    if (gi < o) {
+      const float4 v = acc[gi + o][ci];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      acc[gi][ci] = s;
+    }
+    __syncthreads();
+  }
+  if (gi == 0 && c < d) {
+    Elem<T>::store(dw, c, s.x);
+    Elem<T>::store(dw, c + 1, s.y);
+    Elem<T>::store(dw, c + 2, s.z);
+    Elem<T>::store(dw, c + 3, s.w);
+  }
+}
+
+template <typename T> int norm_waves(int d) {
+  const int per = 64 * kNormPieces * kVec<T>;
+  return d <= per ? 1 : (d <= 4 * per ? 4 : kNormMaxWaves<T>);
+}
+
+// Workgroups of the backward kernel (and parts of dw).
+constexpr int kNormBwdGrid = 1024;
+int norm_bwd_grid(int T, int rows_per_block) {
+  const int blocks = (T + rows_per_block - 1) / rows_per_block;
+  return blocks < kNormBwdGrid ? blocks : kNormBwdGrid;
+}
+
+template <typename T, bool MX> void launch_norm(const NormArgs& a, hipStream_t s) {
+  constexpr int M = kNormMaxWaves<T>;
+  switch (norm_waves<T>(a.d)) {
+    case 1: add_rmsnorm_kernel<T, 1, MX><<<(a.T + 3) / 4, 256, 0, s>>>(a); break;
+    case 4: add_rmsnorm_kernel<T, 4, MX><<<a.T, 256, 0, s>>>(a); break;
+    default: add_rmsnorm_kernel<T, M, MX><<<a.T, 64 * M, 0, s>>>(a);
+  }
+}
+
+template <typename T> int launch_norm_bwd(const NormBwdArgs& a, void* dw, hipStream_t s) {
+  constexpr int M = kNormMaxWaves<T>;
+  const int W = norm_waves<T>(a.d);
+  const int grid = norm_bwd_grid(a.T, W == 1 ? 4 : 1);
+  switch (W) {
+    case 1: rmsnorm_bwd_kernel<T, 1><<<grid, 256, 0, s>>>(a); break;
+    case 4: rmsnorm_bwd_kernel<T, 4><<<grid, 256, 0, s>>>(a); break;
+    default: rmsnorm_bwd_kernel<T, M><<<grid, 64 * M, 0, s>>>(a);
+  }
+  if (int st = launch_status()) return st;
+  if (!dw) return MOE_OK;
+  norm_dw_kernel<T><<<(a.d + kRedCols - 1) / kRedCols, 1024, 0, s>>>(a.part, grid, a.d, static_cast<T*>(dw));
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_add_rmsnorm(int dtype, const void* x, const void* res, const void* w, int T, int d, float eps,
+                               void* h, void* y, void* q, void* s, float* rstd, hipStream_t stream) {
+  MOE_CHECK_ARG(valid_dtype(dtype) && T >= 0 && d > 0 && d % 8 == 0);
+  MOE_CHECK_ARG(eps > 0.0f && eps < INFINITY);
+  MOE_CHECK_ARG((q == nullptr) == (s == nullptr) && (res == nullptr) == (h == nullptr));
+  MOE_CHECK_ARG(q == nullptr || (dtype == MOE_BF16 && d % 128 == 0));
+  MOE_CHECK_ARG(y != nullptr || q != nullptr);
+  MOE_CHECK_SUPPORTED(d <= MOE_MAX_NORM_D);
+  if (T == 0) return MOE_OK;
+  MOE_CHECK_ARG(x && w && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(h) && aligned16(y));
+  MOE_CHECK_ARG(aligned16(q) && aligned4(s) && aligned4(rstd));
+  const NormArgs a{x, res, w, h, y, static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), rstd, T, d, eps};
+  if (dtype == MOE_F32) launch_norm<float, false>(a, stream);
+  else if (q) launch_norm<uint16_t, true>(a, stream);
+  else launch_norm<uint16_t, false>(a, stream);
+  return launch_status();
+}
+
+extern "C" size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int d) {
+  if (T < 1 || d < 1) return 0;
+  // parts of dw: one per workgroup, four rows or more each for short rows
+  return sizeof(float) * (size_t)norm_bwd_grid(T, 1) * d;
+}
+
+extern "C" int moe_add_rmsnorm_bwd(int dtype, const void* dy, const void* h, const void* w, const float* rstd,
+                                   const void* dh, int T, int d, void* dx, void* dw, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  MOE_CHECK_ARG(valid_dtype(dtype) && T >= 0 && d > 0 && d % 8 == 0);
+  MOE_CHECK_SUPPORTED(d <= MOE_MAX_NORM_D);
+  MOE_CHECK_ARG(aligned16(dw));
+  const bool rows = T > 0;
+  MOE_CHECK_ARG(!rows || (dy && h && w && rstd && dx && aligned16(dy) && aligned16(h) && aligned16(w) &&
+                          aligned4(rstd) && aligned16(dh) && aligned16(dx)));
+  if (rows && dw != nullptr && (ws == nullptr || ws_bytes < moe_add_rmsnorm_bwd_workspace_bytes(T, d) || !aligned16(ws)))
+    return MOE_ERR_WORKSPACE;
+  if (!rows) {   // no row: dw is the empty sum
+    if (dw == nullptr) return MOE_OK;
+    const int grid = (d + kRedCols - 1) / kRedCols;
+    if (dtype == MOE_F32) norm_dw_kernel<float><<<grid, 1024, 0, stream>>>(nullptr, 0, d, static_cast<float*>(dw));
+    else norm_dw_kernel<uint16_t><<<grid, 1024, 0, stream>>>(nullptr, 0, d, static_cast<uint16_t*>(dw));
+    return launch_status();
+  }
+  const NormBwdArgs a{dy, h, w, rstd, dh, dx, dw ? static_cast<float*>(ws) : nullptr, T, d};
+  return dtype == MOE_F32 ? launch_norm_bwd<float>(a, dw, stream) : launch_norm_bwd<uint16_t>(a, dw, stream);
+}

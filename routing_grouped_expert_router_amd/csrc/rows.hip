@@ -2,7 +2,7 @@
 // weighted combine, and their adjoints. HBM-bound: one wave per token row,
 // 16-byte loads and stores, every token row read once and every routed row
 // written once. See include/moe.h for the contract of each entry point.
-#include "common.h"
+#include "mx_common.h"
 
 namespace moe {
 
@@ -27,11 +27,6 @@ MOE_DEV int load_row_ids(const int32_t* row_of, size_t t, int k, int n_rows, int
 }
 MOE_DEV int slot_row(int rid, int j) { return __builtin_amdgcn_readlane(rid, j); }
 MOE_DEV float slot_val(float v, int j) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)); }
-
-// Holds a loaded vector in registers from here on. Without it the compiler
-// may move a load down to each of its conditional uses (a store per routed
-// row, an FMA per valid slot) and reload it there, one wait per use.
-MOE_DEV void pin(V16& v) { asm volatile("" : "+v"(v.w[0]), "+v"(v.w[1]), "+v"(v.w[2]), "+v"(v.w[3])); }
 
 // x_perm[row_of[t, j]] = x[t]
 template <typename T>
@@ -68,6 +63,44 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(const T* __restric
     c0 += 64 * kRowUnroll;
     if (c0 - lane >= nvec) break;   // wave-uniform
     load(c0);
+  }
+}
+
+// x[t] = the values of token t's MXFP8 row (codes q, scales s in the grouped
+// layout of T rows) and x_perm[row_of[t, j]] = the same; either output may be
+// null. Reads one byte and writes 2 (k + 1) per value, so the stores bound it:
+// eight values a lane keep each of them a whole 1 KB wave store.
+__global__ void __launch_bounds__(kRowThreads) permute_from_mx_kernel(const uint8_t* __restrict__ q,
+                                                                      const uint8_t* __restrict__ s, int T_, int d,
+                                                                      int k, const int32_t* __restrict__ row_of,
+                                                                      int n_rows, uint16_t* __restrict__ x,
+                                                                      uint16_t* __restrict__ x_perm) {
+  const size_t t = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) >> 6;
+  const int lane = threadIdx.x & 63;
+  if (t >= (size_t)T_) return;
+  const int nvec = d / 8;
+  const uint2* src = reinterpret_cast<const uint2*>(q + t * d);
+  const int rid = x_perm ? load_row_ids(row_of, t, k, n_rows, lane) : -1;
+  for (int c0 = lane; c0 - lane < nvec; c0 += 64 * kRowUnroll) {
+    uint2 cq[kRowUnroll];
+    uint32_t code[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const int c = min(c0 + 64 * u, nvec - 1);
+      cq[u] = src[c];
+      code[u] = s[4 * (static_cast<size_t>(T_) * (c >> 4) + t) + ((c >> 2) & 3)];
+    }
+    V16 v[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) v[u] = decode8(cq[u], code[u]);
+    for (int j = -1; j < k; ++j) {   // j = -1: the token's own row
+      const int r = j < 0 ? 0 : slot_row(rid, j);
+      if (j < 0 ? x == nullptr : r < 0) continue;   // wave-uniform
+      V16* dst = reinterpret_cast<V16*>(j < 0 ? x + t * d : x_perm + (size_t)r * d);
+#pragma unroll
+      for (int u = 0; u < kRowUnroll; ++u)
+        if (c0 + 64 * u < nvec) dst[c0 + 64 * u] = v[u];
+    }
   }
 }
 
@@ -435,6 +468,31 @@ extern "C" int moe_permute(int dtype, const void* x, int T, int d, int k, const 
   else
     permute_kernel<float><<<row_grid(T), kRowThreads, 0, stream>>>(
         static_cast<const float*>(x), T, d, k, row_of, n_rows, static_cast<float*>(x_perm));
+  return launch_status();
+}
+
+extern "C" int moe_permute_from_mx(const void* q, const void* s, int T, int d, int k, const int32_t* row_of,
+                                   const int32_t* src_slot, int n_rows, void* x, void* x_perm, hipStream_t stream) {
+  if (int st = check_rows(MOE_BF16, T, d, k, n_rows)) return st;
+  MOE_CHECK_ARG(d % 128 == 0 && (src_slot || (long)n_rows == (long)T * k));
+  MOE_CHECK_ARG(T == 0 || (q && s && row_of && aligned16(q) && aligned4(s) && aligned16(x)));
+  MOE_CHECK_ARG(n_rows == 0 || (x_perm && aligned16(x_perm)));
+  if (src_slot)
+    if (int st = zero_pads<uint16_t>(src_slot, n_rows, d, x_perm, stream)) return st;
+  if (T == 0) return MOE_OK;
+  permute_from_mx_kernel<<<row_grid(T), kRowThreads, 0, stream>>>(
+      static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), T, d, k, row_of, n_rows,
+      static_cast<uint16_t*>(x), static_cast<uint16_t*>(x_perm));
+  return launch_status();
+}
+
+extern "C" int moe_mx_dequantize(const void* q, const void* s, int rows, int cols, void* dst, hipStream_t stream) {
+  MOE_CHECK_ARG(rows >= 0 && cols > 0 && cols % 128 == 0);
+  if (rows == 0) return MOE_OK;
+  MOE_CHECK_ARG(q && s && dst && aligned16(q) && aligned4(s) && aligned16(dst));
+  permute_from_mx_kernel<<<row_grid(rows), kRowThreads, 0, stream>>>(
+      static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), rows, cols, 0, nullptr, 0,
+      static_cast<uint16_t*>(dst), nullptr);
   return launch_status();
 }
 

@@ -1,0 +1,235 @@
+"""The residual norm, its adjoint and the row restore on the GPU against the
+float64 oracle.
+
+Tolerances. A stored value is off by at most half a step, S = 2^-8 (bf16) or
+2^-24 (binary32) of it. Sums of a row add at most 32 terms in a lane, then 6
+butterfly steps and 12 waves: 50 roundings, so a mean of squares is within
+50 * 2^-24 of itself, rs within half of that and four roundings more.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle.norm import add_rmsnorm, add_rmsnorm_bwd
+from oracle.numerics import (e4m3_decode, f64_to_bf16_bits, mx_dequantize, mx_quantize, round_bf16, round_f32)
+from routing_grouped_expert_router_amd import _lib as L
+
+from parity import dev, host
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+U = 2.0 ** -24
+STEP = {"bf16": 2.0 ** -8, "f32": U}
+TDT = {"bf16": torch.bfloat16, "f32": torch.float32}
+ROUND = {"bf16": round_bf16, "f32": round_f32}
+
+
+def put(a, kind):
+    return dev(f64_to_bf16_bits(a), "bf16") if kind == "bf16" else dev(a.astype(np.float32), "f32")
+
+
+def stored_sum(kind):
+    """x + res as the kernel stores it: a binary32 sum, rounded to the storage type."""
+    return lambda a: ROUND[kind](round_f32(a))
+
+
+def grouped(s):
+    R, nb = s.shape
+    return np.ascontiguousarray(s.reshape(R, nb // 4, 4).transpose(1, 0, 2)).reshape(-1)
+
+
+def inputs(T, d, kind, seed):
+    g = np.random.default_rng([seed, T, d])
+    wide = np.where(g.random(d) < 0.02, 30.0, 1.0)     # a residual stream has a few large channels
+    r = ROUND[kind]
+    x, res = r(g.standard_normal((T, d))), r(g.standard_normal((T, d)) * wide)
+    if T > 2:
+        x[1], res[1] = 0, 0                            # a row of zeros
+        x[2] *= 2.0 ** -70                             # a row whose squares underflow beside eps
+        x[2], res[2] = r(x[2]), 0
+    return x, res, r(1 + 0.2 * g.standard_normal(d)), r(g.standard_normal((T, d))), r(g.standard_normal((T, d)))
+
+
+# one token, odd row counts, widths around each wave count's limit (1024 and
+# 4096 binary32, 2048 and 8192 bf16), the narrowest and the widest
+SHAPES = [(1, 8), (5, 8), (3, 1000), (4, 2048), (7, 2056), (6, 1024), (3, 1032), (2, 4104), (3, 8192), (2, 8200),
+          (1, 12288), (129, 128), (67, 4096)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", SHAPES)
+@pytest.mark.parametrize("with_res", [True, False])
+def test_forward(T, d, kind, with_res):
+    x, res, w, _, _ = inputs(T, d, kind, 1)
+    res = res if with_res else None
+    h_ref, y_ref, rs_ref = add_rmsnorm(x, res, w, EPS, stored_sum(kind))
+    dt = TDT[kind]
+    y, rstd = torch.empty(T, d, dtype=dt, device="cuda"), torch.empty(T, device="cuda")
+    h = torch.empty_like(y) if with_res else None
+    mx = kind == "bf16" and d % 128 == 0
+    q = L.MxTensor(torch.full((T, d), 0xAA, dtype=torch.uint8, device="cuda"),
+                   torch.full((T * d // 32,), 0xAA, dtype=torch.uint8, device="cuda")) if mx else None
+    L.moe_add_rmsnorm(put(x, kind), put(w, kind), EPS, res=None if res is None else put(res, kind), h=h, y=y, q=q,
+                      rstd=rstd)
+    if with_res:
+        assert np.array_equal(host(h), h_ref)
+    assert np.all(np.abs(host(rstd) - rs_ref) <= 30 * U * rs_ref)
+    assert np.all(np.abs(host(y) - y_ref) <= (STEP[kind] + 34 * U) * np.abs(y_ref) + 2.0 ** -133)
+    if mx:   # the copy is the quantiser's of the stored y, bit for bit
+        rq, rs = mx_quantize(host(y))
+        assert np.array_equal(host(q.q), rq) and np.array_equal(host(q.s), grouped(rs))
+        y2 = torch.empty(0, d, dtype=dt, device="cuda")
+        q2 = L.MxTensor(torch.zeros_like(q.q), torch.zeros_like(q.s))
+        L.moe_add_rmsnorm(put(x, kind), put(w, kind), EPS, res=None if res is None else put(res, kind), h=h, q=q2)
+        assert torch.equal(q2.q, q.q) and torch.equal(q2.s, q.s)      # and the same without y
+        assert y2.numel() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(5, 256), (9, 2056), (2, 8200)])
+def test_forward_in_place(T, d, kind):
+    x, res, w, _, _ = inputs(T, d, kind, 2)
+    h0, y0 = (torch.empty(T, d, dtype=TDT[kind], device="cuda") for _ in range(2))
+    L.moe_add_rmsnorm(put(x, kind), put(w, kind), EPS, res=put(res, kind), h=h0, y=y0)
+    X, R = put(x, kind), put(res, kind)
+    L.moe_add_rmsnorm(X, put(w, kind), EPS, res=R, h=R, y=X)          # the stream in place, y over x
+    assert torch.equal(R, h0) and torch.equal(X, y0)
+    X, R = put(x, kind), put(res, kind)
+    L.moe_add_rmsnorm(X, put(w, kind), EPS, res=R, h=X, y=R)          # h over x
+    assert torch.equal(X, h0)
+    X = h0.clone()
+    L.moe_add_rmsnorm(X, put(w, kind), EPS, y=X)                      # no residual, y over x
+    assert torch.equal(X, y0)
+
+
+def test_rows_are_independent():
+    """A row with infinities or NaN leaves the others as they are."""
+    x, res, w, _, _ = inputs(9, 512, "bf16", 3)
+    X, W = put(x, "bf16"), put(w, "bf16")
+    y0, y1 = torch.empty_like(X), torch.empty_like(X)
+    L.moe_add_rmsnorm(X, W, EPS, y=y0)
+    X[4, 7], X[6, 0] = float("nan"), float("inf")
+    L.moe_add_rmsnorm(X, W, EPS, y=y1)
+    keep = [i for i in range(9) if i not in (4, 6)]
+    assert torch.equal(y0[keep], y1[keep])
+    assert bool(y1[4].isnan().all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", SHAPES + [(4500, 64), (1025, 264), (2051, 2056)])
+@pytest.mark.parametrize("with_dh", [True, False])
+def test_backward(T, d, kind, with_dh):
+    x, res, w, dy, dh = inputs(T, d, kind, 4)
+    h = ROUND[kind](x + res)
+    rs = round_f32(1 / np.sqrt(np.mean(h * h, axis=1) + EPS))
+    dh = dh if with_dh else None
+    dx_ref, dw_ref = add_rmsnorm_bwd(dy, h, w, rs, dh)
+    dt = TDT[kind]
+    dx, dw = torch.empty(T, d, dtype=dt, device="cuda"), torch.empty(d, dtype=dt, device="cuda")
+    ws = torch.empty(max(L.moe_add_rmsnorm_bwd_workspace_bytes(T, d), 16), dtype=torch.uint8, device="cuda")
+    args = (put(dy, kind), put(h, kind), put(w, kind), dev(rs.astype(np.float32), "f32"), dx)
+    DH = None if dh is None else put(dh, kind)
+    L.moe_add_rmsnorm_bwd(*args, dw=dw, dh=DH, ws=ws)
+    n, g = np.abs(h * rs[:, None]), np.abs(dy * w)
+    # the row's dot product takes 50 roundings of sum |g n|, each term and the result a few more
+    tol = 60 * U * rs[:, None] * (g + n * np.mean(g * n, axis=1, keepdims=True))
+    if dh is not None:
+        tol = tol + 2 * U * (np.abs(dh) + np.abs(dx_ref))
+    assert np.all(np.abs(host(dx) - dx_ref) <= STEP[kind] * (np.abs(dx_ref) + tol) + tol + 2.0 ** -133)
+    # a column's sum: T / 4096 or T / 1024 rows in a thread, 4 waves, 16 parts, 6 steps
+    tol = (T / 1024 + 30) * U * np.sum(np.abs(dy) * n, axis=0)
+    assert np.all(np.abs(host(dw) - dw_ref) <= STEP[kind] * (np.abs(dw_ref) + tol) + tol + 2.0 ** -133)
+    # the same bits again, without dw, and with dx over dy or over dh
+    first, fw = dx.clone(), dw.clone()
+    L.moe_add_rmsnorm_bwd(*args, dw=dw, dh=DH, ws=ws)
+    assert torch.equal(dx, first) and torch.equal(dw, fw)
+    dx.zero_()
+    L.moe_add_rmsnorm_bwd(*args, dh=DH)
+    assert torch.equal(dx, first)
+    over = args[0].clone()
+    L.moe_add_rmsnorm_bwd(over, *args[1:4], over, dw=dw, dh=DH, ws=ws)
+    assert torch.equal(over, first) and torch.equal(dw, fw)
+    if dh is not None:
+        L.moe_add_rmsnorm_bwd(*args[:4], DH, dw=dw, dh=DH, ws=ws)
+        assert torch.equal(DH, first)
+
+
+def test_backward_without_rows():
+    dw = torch.full((264,), 7.0, dtype=torch.bfloat16, device="cuda")
+    e = torch.empty(0, 264, dtype=torch.bfloat16, device="cuda")
+    L.moe_add_rmsnorm_bwd(e, e, dw, torch.empty(0, device="cuda"), e, dw=dw)
+    assert not host(dw).any()
+
+
+def test_backward_is_the_forward_kernels_difference_quotient():
+    """Central differences of the binary32 forward along random directions:
+    the outputs carry 40 * 2^-24 of themselves, over 2 e = 2^-5; the third
+    derivative along a unit-variance direction is below 6 |y|-ish terms times
+    e^2 / 6 = 2^-13."""
+    T, d, e = 16, 512, 2.0 ** -6
+    x, res, w, dy, dh = inputs(T, d, "f32", 5)
+    x[1] = x[0]
+    x[2] = x[3]
+    g = np.random.default_rng(6)
+    v = round_f32(g.standard_normal((T, d)))
+
+    def loss(a):
+        h, y = (torch.empty(T, d, device="cuda") for _ in range(2))
+        L.moe_add_rmsnorm(put(round_f32(a), "f32"), put(w, "f32"), EPS, res=put(res, "f32"), h=h, y=y)
+        return (dy * host(y)).sum(1) + (dh * host(h)).sum(1), np.abs(dy * host(y)).sum(1) + np.abs(dh * host(h)).sum(1)
+
+    (up, mag), (down, _) = loss(x + e * v), loss(x - e * v)
+    h, y, rstd = torch.empty(T, d, device="cuda"), torch.empty(T, d, device="cuda"), torch.empty(T, device="cuda")
+    L.moe_add_rmsnorm(put(x, "f32"), put(w, "f32"), EPS, res=put(res, "f32"), h=h, y=y, rstd=rstd)
+    dx = torch.empty_like(h)
+    L.moe_add_rmsnorm_bwd(put(dy, "f32"), h, put(w, "f32"), rstd, dx, dh=put(dh, "f32"))
+    got = (host(dx) * v).sum(1)
+    assert np.all(np.abs((up - down) / (2 * e) - got) <= mag * (40 * U / e + 2.0 ** -11))
+
+
+# ----------------------------------------------------------------------------- restore
+def test_dequantize_every_code_and_scale():
+    """Every finite code under every scale, exact where the product is a bf16 value."""
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], dtype=np.uint8)
+    q = np.zeros((255, 256), dtype=np.uint8)
+    q[:, :254] = codes
+    s = np.repeat(np.arange(255, dtype=np.uint8)[:, None], 8, axis=1)
+    dst = torch.empty(255, 256, dtype=torch.bfloat16, device="cuda")
+    L.moe_mx_dequantize(L.MxTensor(dev(q, "u8"), dev(grouped(s), "u8")), dst)
+    with np.errstate(over="ignore"):
+        want = np.ldexp(e4m3_decode(q), s.astype(int)[:, :1] - 127)
+        want = round_bf16(want)
+    assert np.array_equal(host(dst), want)
+
+
+@pytest.mark.parametrize("T,d,k,E,cap", [(1, 128, 1, 1, 0), (1, 2048, 4, 16, 0), (333, 384, 2, 8, 0),
+                                         (65, 2176, 3, 8, 0), (130, 4224, 16, 32, 0), (300, 256, 2, 8, 40)])
+def test_permute_from_mx(T, d, k, E, cap):
+    g = np.random.default_rng([7, T, d])
+    x = round_bf16(g.standard_normal((T, d)) * np.exp2(g.integers(-20, 20, (T, 1))))
+    idx = dev(np.stack([g.permutation(E)[:k] for _ in range(T)]).astype(np.int32), "i32")
+    n = E * cap if cap else T * k
+    i32 = lambda m: torch.empty(m, dtype=torch.int32, device="cuda")
+    row_of, src_slot, off = i32(T * k), i32(n), i32(E + 1)
+    ws = i32(max(L.moe_offsets_workspace_bytes(T, k, E) // 4, 4))
+    L.moe_offsets(idx, E, cap, i32(E), off, row_of, src_slot, i32(1), torch.zeros(1, dtype=torch.int32, device="cuda"), ws)
+    q = L.MxTensor(torch.empty(T, d, dtype=torch.uint8, device="cuda"),
+                   torch.empty(T * d // 32, dtype=torch.uint8, device="cuda"))
+    L.moe_mx_quantize(put(x, "bf16"), 0, q.q, q.s)
+    out, x_perm, want = (torch.full((m, d), 3.0, dtype=torch.bfloat16, device="cuda") for m in (T, n, n))
+    L.moe_permute_from_mx(q, k, row_of, src_slot if cap else None, x_perm, x=out)
+    assert np.array_equal(host(out), mx_dequantize(*mx_quantize(x)))
+    L.moe_permute(out, k, row_of, src_slot if cap else None, want)
+    assert torch.equal(x_perm, want)
+    again = torch.full_like(x_perm, 5.0)
+    L.moe_permute_from_mx(q, k, row_of, src_slot if cap else None, again)
+    assert torch.equal(again, want)
+    if not cap:     # a row id outside the buffer is skipped, its row left as it was
+        bad = row_of.clone()
+        r = int(bad[0])
+        bad[0] = -1
+        again.fill_(5.0)
+        L.moe_permute_from_mx(q, k, bad, None, again)
+        want[r] = 5.0
+        assert torch.equal(again, want)
