@@ -325,6 +325,32 @@ typedef struct moe_gg_desc {
 size_t moe_grouped_gemm_workspace_bytes(const moe_gg_desc* desc);
 int moe_grouped_gemm(const moe_gg_desc* desc, hipStream_t stream);
 
+typedef struct moe_mx_tensor {
+  const void* q;   /* E4M3 codes */
+  const void* s;   /* E8M0 scales */
+} moe_mx_tensor;
+
+/* moe_grouped_gemm_ckpt: the two GEMMs around the activations that a layer
+ * holds from its forward to its backward pass, with G and U held in 8 bits:
+ * as MXFP8 rows (the format and layout of moe_mx_quantize axis 0: codes
+ * [n_rows, F], scales of n_rows * F / 32 bytes), 66 bytes where bf16 g and u
+ * take 128.
+ *   MOE_GG_FWD_GATE_UP  writes h from the rounded bf16 g and u, as
+ *                       moe_grouped_gemm does, and the copies *g and *u of
+ *                       those bf16 values in place of g and u;
+ *   MOE_GG_DGRAD_DOWN   reads the copies: with g, u their values, dg and du
+ *                       as in moe_grouped_gemm, and, where desc->h is not
+ *                       NULL, h = silu(g) * u for MOE_GG_WGRAD_DOWN, so that
+ *                       the forward's h need not be held either.
+ * The gradients are those of the forward at the copies' values: G and U each
+ * carry one rounding to E4M3 under a shared scale (half a step, 2^-4 of the
+ * value for normal codes). desc->g and desc->u must be NULL; other fields as
+ * for moe_grouped_gemm. bf16 with d and F multiples of 256 only (else
+ * MOE_ERR_UNSUPPORTED). Rows outside every group are neither read nor
+ * written. */
+int moe_grouped_gemm_ckpt(const moe_gg_desc* desc, const moe_mx_tensor* g, const moe_mx_tensor* u,
+                          hipStream_t stream);
+
 /* ----------------------------------------------------------------- MXFP8
  * The pages credit MXFP8 for most of the feed-forward speed-up (bigchange.ai
  * pt-BR, "Três números, três denominadores"; unite.ai/hi, "पैरालेलिज़्म,
@@ -432,11 +458,6 @@ int moe_permute_from_mx(const void* q, const void* s, int T, int d, int k, const
  * writes there the tile split of moe_grouped_gemm's weight gradients and each
  * expert's first padded token column; the other ops need none. Calls sharing
  * one workspace must be ordered on one stream. */
-typedef struct moe_mx_tensor {
-  const void* q;   /* E4M3 codes */
-  const void* s;   /* E8M0 scales */
-} moe_mx_tensor;
-
 typedef struct moe_mx_gg_desc {
   int op;                        /* moe_gg_op */
   int E, d, F;
@@ -466,6 +487,14 @@ typedef struct moe_mx_gg_desc {
 
 size_t moe_grouped_gemm_mx_workspace_bytes(const moe_mx_gg_desc* desc);
 int moe_grouped_gemm_mx(const moe_mx_gg_desc* desc, hipStream_t stream);
+
+/* moe_grouped_gemm_mx_ckpt: moe_grouped_gemm_ckpt for the MXFP8 GEMMs:
+ * FWD_GATE_UP writes the copies *g and *u instead of out0 and out1 (which must
+ * be NULL), DGRAD_DOWN reads them instead of desc->g and desc->u (NULL). The
+ * MXFP8 layer keeps H as its weight gradient's operand, so no h is written
+ * again. Everything else as for moe_grouped_gemm_mx. */
+int moe_grouped_gemm_mx_ckpt(const moe_mx_gg_desc* desc, const moe_mx_tensor* g, const moe_mx_tensor* u,
+                             hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -72,6 +72,7 @@ SIGNATURES = {
     "moe_router_gemm_bwd": (_i, [_i, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "moe_grouped_gemm_workspace_bytes": (_sz, [C.POINTER(moe_gg_desc)]),
     "moe_grouped_gemm": (_i, [C.POINTER(moe_gg_desc), _vp]),
+    "moe_grouped_gemm_ckpt": (_i, [C.POINTER(moe_gg_desc), C.POINTER(moe_mx_tensor), C.POINTER(moe_mx_tensor), _vp]),
     "moe_mx_col_stride": (_i, [_i, _i]),
     "moe_mx_quantize": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp]),
     "moe_mx_quantize_both": (_i, [_vp, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
@@ -80,6 +81,8 @@ SIGNATURES = {
     "moe_permute_from_mx": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp]),
     "moe_grouped_gemm_mx_workspace_bytes": (_sz, [C.POINTER(moe_mx_gg_desc)]),
     "moe_grouped_gemm_mx": (_i, [C.POINTER(moe_mx_gg_desc), _vp]),
+    "moe_grouped_gemm_mx_ckpt": (_i, [C.POINTER(moe_mx_gg_desc), C.POINTER(moe_mx_tensor), C.POINTER(moe_mx_tensor),
+                                      _vp]),
 }
 
 _lib: Optional[C.CDLL] = None
@@ -400,6 +403,20 @@ def moe_grouped_gemm(desc: moe_gg_desc, stream=None):
     _call("moe_grouped_gemm", C.byref(desc), _stream(stream))
 
 
+def _ckpt(desc, g: MxTensor, u: MxTensor):
+    """The 8-bit rows of G and U as descriptors, checked against desc's sizes."""
+    n, u8 = desc.n_rows * desc.F, torch.uint8
+    _same_device(g.q, g.s, u.q, u.s)
+    mg, mu = moe_mx_tensor(), moe_mx_tensor()
+    _fill(None, [((m, f), _req(getattr(t, f), f"{name}.{f}", u8, min_numel=size))
+                 for m, t, name in ((mg, g, "g"), (mu, u, "u")) for f, size in (("q", n), ("s", n // 32))])
+    return C.byref(mg), C.byref(mu)
+
+
+def moe_grouped_gemm_ckpt(desc: moe_gg_desc, g: MxTensor, u: MxTensor, stream=None):
+    _call("moe_grouped_gemm_ckpt", C.byref(desc), *_ckpt(desc, g, u), _stream(stream))
+
+
 # ----------------------------------------------------------------- MXFP8
 def moe_mx_col_stride(rows: int, n_groups: int) -> int:
     return lib().moe_mx_col_stride(rows, n_groups)
@@ -481,3 +498,7 @@ def moe_grouped_gemm_mx_workspace_bytes(desc: moe_mx_gg_desc) -> int:
 
 def moe_grouped_gemm_mx(desc: moe_mx_gg_desc, stream=None):
     _call("moe_grouped_gemm_mx", C.byref(desc), _stream(stream))
+
+
+def moe_grouped_gemm_mx_ckpt(desc: moe_mx_gg_desc, g: MxTensor, u: MxTensor, stream=None):
+    _call("moe_grouped_gemm_mx_ckpt", C.byref(desc), *_ckpt(desc, g, u), _stream(stream))

@@ -241,6 +241,16 @@ int launch_dma(const moe_gg_desc* g, const GGArgs& a, bool kvar, bool dual, int 
   return dispatch_op<Dma<C>::template Launch>(g->op, a, static_cast<int>(grid), stream);
 }
 
+// The two ops that keep G and U in 8 bits (N / bno column tiles).
+int launch_ckpt(const moe_gg_desc* g, const GGArgs& a, int tiles_n, hipStream_t stream) {
+  using C = WithCkpt<CfgDma>;
+  const long grid = ((g->n_rows + C::BM - 1) / C::BM + g->E) * (long)tiles_n;
+  MOE_CHECK_SUPPORTED(grid < (1L << 31));
+  if (g->op == MOE_GG_FWD_GATE_UP) gg_dma_kernel<MOE_GG_FWD_GATE_UP, C><<<(int)grid, C::NT, 0, stream>>>(a);
+  else gg_dma_kernel<MOE_GG_DGRAD_DOWN, C><<<(int)grid, C::NT, 0, stream>>>(a);
+  return launch_status();
+}
+
 template <int OP> struct LaunchSimpleBf16 {
   static void go(const GGArgs& a, int grid, hipStream_t s) {
     gg_simple_kernel<uint16_t, OP><<<grid, 256, 0, s>>>(a);
@@ -295,7 +305,9 @@ extern "C" size_t moe_grouped_gemm_workspace_bytes(const moe_gg_desc* desc) {
   return ks > 1 ? kPartialOffset + splitk_bytes(desc, ks) : kSplitBytes;
 }
 
-extern "C" int moe_grouped_gemm(const moe_gg_desc* g, hipStream_t stream) {
+namespace {
+// ck: null, or the 8-bit rows of G and U (FWD_GATE_UP and DGRAD_DOWN only)
+int grouped_gemm(const moe_gg_desc* g, const moe_mx_tensor* const* ck, hipStream_t stream) {
   MOE_CHECK_ARG(g != nullptr);
   MOE_CHECK_ARG(valid_dtype(g->dtype) && g->op >= MOE_GG_FWD_GATE_UP && g->op <= MOE_GG_WGRAD_GATE_UP);
   MOE_CHECK_ARG(g->E >= 1 && g->d > 0 && g->F > 0 && g->n_rows >= 0 && g->capacity >= 0);
@@ -314,14 +326,15 @@ extern "C" int moe_grouped_gemm(const moe_gg_desc* g, hipStream_t stream) {
   switch (g->op) {
     case MOE_GG_FWD_GATE_UP:
       MOE_CHECK_ARG(need(g->x_perm) && need(g->w_gate) && need(g->w_up) && need(g->h));
-      // g and u both written, or both NULL (only h is wanted)
+      // g and u both written, or both NULL (only h is wanted, or they are kept in 8 bits)
       MOE_CHECK_ARG((need(g->g) && need(g->u)) || (g->g == nullptr && g->u == nullptr));
       break;
     case MOE_GG_FWD_DOWN:
       MOE_CHECK_ARG(need(g->h) && need(g->w_down) && need(g->y_perm));
       break;
     case MOE_GG_DGRAD_DOWN:
-      MOE_CHECK_ARG(need(g->dy_perm) && need(g->w_down) && need(g->g) && need(g->u) && need(g->dg) && need(g->du));
+      MOE_CHECK_ARG(need(g->dy_perm) && need(g->w_down) && need(g->dg) && need(g->du));
+      MOE_CHECK_ARG(ck ? aligned16(g->h) : need(g->g) && need(g->u));
       break;
     case MOE_GG_DGRAD_GATE_UP:
       MOE_CHECK_ARG(need(g->dg) && need(g->du) && need(g->w_gate) && need(g->w_up) && need(g->dx_perm));
@@ -353,6 +366,13 @@ extern "C" int moe_grouped_gemm(const moe_gg_desc* g, hipStream_t stream) {
     // must span less than 2 GiB
     const long span = (long)g->n_rows * (g->d > g->F ? g->d : g->F) * 2;
     MOE_CHECK_SUPPORTED(span < (1L << 31) && (long)g->d * g->F * 2 < (1L << 31));
+    if (ck) {
+      for (int i = 0; i < 2; ++i) {
+        a.ckq[i] = static_cast<uint8_t*>(const_cast<void*>(ck[i]->q));
+        a.cks[i] = static_cast<uint8_t*>(const_cast<void*>(ck[i]->s));
+      }
+      return launch_ckpt(g, a, N / (dual ? CfgDma::BN / 2 : CfgDma::BN), stream);
+    }
     return launch_dma<CfgDma>(g, a, kvar, dual, N, stream);
   }
   long grid;
@@ -362,4 +382,20 @@ extern "C" int moe_grouped_gemm(const moe_gg_desc* g, hipStream_t stream) {
   MOE_CHECK_SUPPORTED(grid < (1L << 31));
   if (g->dtype == MOE_BF16) return dispatch_op<LaunchSimpleBf16>(g->op, a, static_cast<int>(grid), stream);
   return dispatch_op<LaunchSimpleF32>(g->op, a, static_cast<int>(grid), stream);
+}
+}  // namespace
+
+extern "C" int moe_grouped_gemm(const moe_gg_desc* g, hipStream_t stream) { return grouped_gemm(g, nullptr, stream); }
+
+extern "C" int moe_grouped_gemm_ckpt(const moe_gg_desc* desc, const moe_mx_tensor* g, const moe_mx_tensor* u,
+                                     hipStream_t stream) {
+  MOE_CHECK_ARG(desc != nullptr && g != nullptr && u != nullptr);
+  MOE_CHECK_ARG(desc->op == MOE_GG_FWD_GATE_UP || desc->op == MOE_GG_DGRAD_DOWN);
+  MOE_CHECK_ARG(desc->g == nullptr && desc->u == nullptr);
+  MOE_CHECK_ARG(desc->n_rows <= 0 || (g->q && g->s && u->q && u->s && aligned16(g->q) && aligned16(u->q) &&
+                                      aligned4(g->s) && aligned4(u->s)));
+  MOE_CHECK_ARG(valid_dtype(desc->dtype) && desc->d > 0 && desc->F > 0);
+  MOE_CHECK_SUPPORTED(mfma_ok(desc));
+  const moe_mx_tensor* ck[2] = {g, u};
+  return grouped_gemm(desc, ck, stream);
 }

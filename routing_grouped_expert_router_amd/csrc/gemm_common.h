@@ -47,6 +47,16 @@ struct GGArgs {
   // fixed order by gg_splitk_reduce_kernel; null and 0 otherwise
   float* partial;
   int ksplit;
+  // G and U as MXFP8 rows (codes and scales in the grouped layout of n_rows
+  // rows) in place of bf16 g and u: written by FWD_GATE_UP, read by
+  // DGRAD_DOWN of the configurations with kCkpt; unused elsewhere
+  uint8_t* ckq[2];
+  uint8_t* cks[2];
+};
+
+// A tile configuration whose epilogue keeps G and U in 8 bits (GGArgs::ckq).
+template <class C> struct WithCkpt : C {
+  static constexpr bool kCkpt = true;
 };
 
 // Static shape of each op as C[M x N] = sum_k A[m, k] B[k, n] per expert.

@@ -82,6 +82,32 @@ MOE_DEV void mx_quantize_plane(const uint16_t* stg, const MxQOut& o, size_t grow
   }
 }
 
+// G (which = 0) or U (1) kept in 8 bits between the passes, as MXFP8 rows
+// written the way moe_mx_quantize axis 0 writes them: half the bytes of the
+// bf16 tensors in each direction, one rounding to E4M3 of the bf16 value.
+//
+// ckpt_put: eight consecutive columns col.. of permuted row `row`; the 16
+// lanes of an aligned group hold columns 128k.. in order (c: 0..15, the lane's
+// place), four lanes one block, and lane 0 stores the group's scale word.
+MOE_DEV void ckpt_put(const GGArgs& a, int which, size_t row, int col, int c, const V16& v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = mag_max2(m, v.w[i]);
+  m = max2(m, __shfl_xor(m, 1, 64));
+  m = max2(m, __shfl_xor(m, 2, 64));
+  const BlockScale bs = block_scale(max_half(m));
+  *reinterpret_cast<uint2*>(a.ckq[which] + row * a.F + col) =
+      make_uint2(encode_quad(v.w[0], v.w[1], bs), encode_quad(v.w[2], v.w[3], bs));
+  const uint32_t code = static_cast<uint32_t>(bs.x + 127);
+  const uint32_t word = code | __shfl_down(code, 4, 64) << 8 | __shfl_down(code, 8, 64) << 16 |
+                        __shfl_down(code, 12, 64) << 24;
+  if (c == 0) *reinterpret_cast<uint32_t*>(a.cks[which] + 4 * ((size_t)a.n_rows * (col / 128) + row)) = word;
+}
+MOE_DEV V16 ckpt_get(const GGArgs& a, int which, size_t row, int col) {
+  const uint2 q = *reinterpret_cast<const uint2*>(a.ckq[which] + row * a.F + col);
+  return decode8(q, a.cks[which][4 * ((size_t)a.n_rows * (col / 128) + row) + (col / 32 & 3)]);
+}
+
 // Each 32x32 block of acc holds C^T (B fragment first): lane (lr, lk) has
 // tile row wm*WMR + mi*32 + lr and, for accumulator group g, the 4
 // consecutive columns 8g + 4lk .. +3 of block ni. Output columns are handled
@@ -195,7 +221,10 @@ MOE_DEV void gg_store_tile(const GGArgs& a, const df32x16_t (&acc)[C::MI][C::NI]
         const V16 gv = *reinterpret_cast<const V16*>(stg0 + r * LDW + c * 8);
         const V16 uv = *reinterpret_cast<const V16*>(stg1 + r * LDW + c * 8);
         const size_t o = (size_t)r * F + c * 8;
-        if (keep_gu) {
+        if constexpr (C::kCkpt) {   // 16 lanes hold the 128 columns of one scale word
+          ckpt_put(a, 0, rbase + r, n0 + c * 8, c, gv);
+          ckpt_put(a, 1, rbase + r, n0 + c * 8, c, uv);
+        } else if (keep_gu) {
           *reinterpret_cast<V16*>(outg + o) = gv;
           *reinterpret_cast<V16*>(outu + o) = uv;
         }
@@ -221,8 +250,30 @@ MOE_DEV void gg_store_tile(const GGArgs& a, const df32x16_t (&acc)[C::MI][C::NI]
   } else if (OP == MOE_GG_DGRAD_DOWN) {
     // per column chunk: stage G and U, turn them into dG and dU in place
     for (int ch = 0; ch < NCH; ++ch) {
-      load_plane(stg0, (const uint16_t*)a.g + rbase * F + n0, F, ch);
-      load_plane(stg1, (const uint16_t*)a.u + rbase * F + n0, F, ch);
+      if constexpr (C::kCkpt) {
+        // G and U from their 8-bit rows; H, wanted again by the weight
+        // gradient, from the same values
+        constexpr int CPRW = CW / 8;
+        uint16_t* outh = (uint16_t*)a.h + rbase * F + n0 + ch * CW;
+        for (int q = tid; q < rows_valid * CPRW; q += NT) {
+          const int r = q / CPRW, c = q % CPRW;
+          const V16 gv = ckpt_get(a, 0, rbase + r, n0 + ch * CW + c * 8);
+          const V16 uv = ckpt_get(a, 1, rbase + r, n0 + ch * CW + c * 8);
+          *reinterpret_cast<V16*>(stg0 + r * LDW + c * 8) = gv;
+          *reinterpret_cast<V16*>(stg1 + r * LDW + c * 8) = uv;
+          if (a.h != nullptr) {
+            float gf[8], uf[8];
+            unpack(gv, gf);
+            unpack(uv, uf);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gf[i] = gf[i] * uf[i] * fast_sigmoid(gf[i]);
+            *reinterpret_cast<V16*>(outh + (size_t)r * F + c * 8) = pack(gf);
+          }
+        }
+      } else {
+        load_plane(stg0, (const uint16_t*)a.g + rbase * F + n0, F, ch);
+        load_plane(stg1, (const uint16_t*)a.u + rbase * F + n0, F, ch);
+      }
       __syncthreads();
       if (wchunk == ch) {
 #pragma unroll

@@ -50,7 +50,9 @@ extern "C" size_t moe_grouped_gemm_mx_workspace_bytes(const moe_mx_gg_desc* desc
   return kvar ? sizeof(int) * (size_t)(kMxColStart + E) : 0;
 }
 
-extern "C" int moe_grouped_gemm_mx(const moe_mx_gg_desc* g, hipStream_t stream) {
+namespace {
+// ck: null, or the 8-bit rows of G and U (FWD_GATE_UP and DGRAD_DOWN only)
+int grouped_gemm_mx(const moe_mx_gg_desc* g, const moe_mx_tensor* const* ck, hipStream_t stream) {
   MOE_CHECK_ARG(g != nullptr);
   MOE_CHECK_ARG(g->op >= MOE_GG_FWD_GATE_UP && g->op <= MOE_GG_WGRAD_GATE_UP);
   MOE_CHECK_ARG(g->E >= 1 && g->d > 0 && g->F > 0 && g->n_rows >= 0 && g->group_offsets != nullptr);
@@ -70,7 +72,8 @@ extern "C" int moe_grouped_gemm_mx(const moe_mx_gg_desc* g, hipStream_t stream) 
     case MOE_GG_FWD_GATE_UP:
       MOE_CHECK_ARG(tensor_ok(g->a0) && tensor_ok(g->b0) && tensor_ok(g->b1));
       // H in bf16 may be left out when its MXFP8 copies are written
-      MOE_CHECK_ARG(out_ok(g->out0) && out_ok(g->out1) && (out_ok(g->out2) || (qo && g->out2 == nullptr)));
+      MOE_CHECK_ARG(ck || (out_ok(g->out0) && out_ok(g->out1)));
+      MOE_CHECK_ARG((out_ok(g->out2) || (qo && g->out2 == nullptr)));
       span = span > F * E * d ? span : F * E * d;
       break;
     case MOE_GG_FWD_DOWN:
@@ -81,7 +84,7 @@ extern "C" int moe_grouped_gemm_mx(const moe_mx_gg_desc* g, hipStream_t stream) 
       // dG and dU in bf16 may be left out (both) when their MXFP8 copies are written
       MOE_CHECK_ARG(tensor_ok(g->a0) && tensor_ok(g->b0));
       MOE_CHECK_ARG((out_ok(g->out0) && out_ok(g->out1)) || (qo && g->out0 == nullptr && g->out1 == nullptr));
-      MOE_CHECK_ARG(out_ok(g->g) && out_ok(g->u));
+      MOE_CHECK_ARG(ck || (out_ok(g->g) && out_ok(g->u)));
       break;
     case MOE_GG_DGRAD_GATE_UP:
       MOE_CHECK_ARG(tensor_ok(g->a0) && tensor_ok(g->a1) && tensor_ok(g->b0) && tensor_ok(g->b1));
@@ -151,5 +154,31 @@ extern "C" int moe_grouped_gemm_mx(const moe_mx_gg_desc* g, hipStream_t stream) 
   if (kvar) grid = E * (op_wgrad_m(g->op, g->d, g->F) / CfgMx::BM) * (N / bno);
   else grid = ((g->n_rows + CfgMx::BM - 1) / CfgMx::BM + E) * (long)(N / bno);
   MOE_CHECK_SUPPORTED(grid < (1L << 31));
+  if (ck) {
+    for (int i = 0; i < 2; ++i) {
+      x.o.ckq[i] = static_cast<uint8_t*>(const_cast<void*>(ck[i]->q));
+      x.o.cks[i] = static_cast<uint8_t*>(const_cast<void*>(ck[i]->s));
+    }
+    using C = WithCkpt<CfgMx>;
+    if (g->op == MOE_GG_FWD_GATE_UP) gg_mx_kernel<MOE_GG_FWD_GATE_UP, C><<<(int)grid, C::NT, 0, stream>>>(x);
+    else gg_mx_kernel<MOE_GG_DGRAD_DOWN, C><<<(int)grid, C::NT, 0, stream>>>(x);
+    return launch_status();
+  }
   return launch_mx(g->op, x, static_cast<int>(grid), stream);
+}
+}  // namespace
+
+extern "C" int moe_grouped_gemm_mx(const moe_mx_gg_desc* g, hipStream_t stream) {
+  return grouped_gemm_mx(g, nullptr, stream);
+}
+
+extern "C" int moe_grouped_gemm_mx_ckpt(const moe_mx_gg_desc* desc, const moe_mx_tensor* g, const moe_mx_tensor* u,
+                                        hipStream_t stream) {
+  MOE_CHECK_ARG(desc != nullptr && g != nullptr && u != nullptr);
+  MOE_CHECK_ARG(desc->op == MOE_GG_FWD_GATE_UP || desc->op == MOE_GG_DGRAD_DOWN);
+  MOE_CHECK_ARG(desc->n_rows <= 0 || (tensor_ok(*g) && tensor_ok(*u)));
+  if (desc->op == MOE_GG_FWD_GATE_UP) MOE_CHECK_ARG(desc->out0 == nullptr && desc->out1 == nullptr);
+  else MOE_CHECK_ARG(desc->g == nullptr && desc->u == nullptr);
+  const moe_mx_tensor* ck[2] = {g, u};
+  return grouped_gemm_mx(desc, ck, stream);
 }

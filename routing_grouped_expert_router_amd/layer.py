@@ -37,6 +37,17 @@ deniz.in, "Ai2'nin raporladığı sayılar"; unite.ai/hi, "पैरालेल
 और मेमोरी तकनीकें"). The recomputed values are bitwise those of the forward
 (the kernels are deterministic).
 
+With ``act8=True`` (bf16 tensors, d and F multiples of 256) what the forward
+leaves for the backward is held in 8 bits: the layer's input as MXFP8 token
+rows (the ``x8`` the caller's norm wrote, or quantised here), G and U as MXFP8
+rows written by the gate/up GEMM's epilogue. x_perm and H are scratch of the
+forward; the backward rebuilds x and x_perm from the input's copy and H from
+the copies of G and U, which the data-gradient GEMM reads in its epilogue. No
+GEMM runs twice. The gradients are those at the copies' values (E4M3 under a
+shared scale per 32 values); y is the bf16 layer's, bit for bit. With
+``mxfp8=True`` as well, the permuted input is held in the GEMMs' own operands
+and H likewise, so only G, U and the router's input change.
+
 Memory: routing metadata and workspaces are allocated with the layer; the
 tensors the forward writes (x_perm, y_perm, y and, without recompute, G, U,
 H) are allocated by the first forward and the gradient buffers by the first
@@ -60,7 +71,8 @@ class MoELayer:
     def __init__(self, T: int, d: int, E: int, k: int, F: int, dtype=torch.bfloat16,
                  routing: str = "learned", capacity: int = 0, backward: bool = True,
                  device: str = "cuda", recompute: bool = False, shared_ff: int = 0,
-                 mxfp8: bool = False, keep_intermediates: bool = True, mx_bf16_intermediates: bool = True):
+                 mxfp8: bool = False, keep_intermediates: bool = True, mx_bf16_intermediates: bool = True,
+                 act8: bool = False):
         if routing not in ("learned", "given"):
             raise ValueError(routing)
         self.T, self.d, self.E, self.k, self.F = T, d, E, k, F
@@ -104,6 +116,10 @@ class MoELayer:
         self.x_perm = self.g = self.u = self.h = self.y_perm = self.y = None
         self.dy_perm = self.dtopk_w = self.dg = self.du = self.dx_perm = self.dx = None
         self.dw_gate = self.dw_up = self.dw_down = self.dlogits = self.dw_r = None
+        self.act8 = act8
+        self.x8 = self._x8 = self.g8 = self.u8 = self.g8_s = self.u8_s = None
+        if act8 and (recompute or dtype != torch.bfloat16 or d % 256 or F % 256 or shared_ff % 256):
+            raise ValueError("act8 needs bf16 with d, F and shared_ff multiples of 256, without recompute")
         self.mxfp8 = mxfp8
         if mxfp8:
             if capacity > 0 or dtype != torch.bfloat16 or recompute or shared_ff > 0:
@@ -115,7 +131,9 @@ class MoELayer:
         if shared_ff > 0:
             Fs = shared_ff
             self.offsets_s = torch.tensor([0, T], dtype=i32, device=dev)
-            self.g_s, self.u_s, self.h_s = e(T, Fs), e(T, Fs), e(T, Fs)
+            self.g_s = self.u_s = self.h_s = None
+            if not act8:
+                self.g_s, self.u_s, self.h_s = e(T, Fs), e(T, Fs), e(T, Fs)
             self.y_s = e(T, d)
             if backward:
                 self.dg_s, self.du_s = e(T, Fs), e(T, Fs)
@@ -134,15 +152,23 @@ class MoELayer:
         writes quantised rows only), y_perm, y and, unless recomputing, G, U, H."""
         nr, d, F = self.n_rows, self.d, self.F
         if self.y is None:
-            if not self.mxfp8:
+            if not self.mxfp8 and not self.act8:
                 self.x_perm = self._new(nr, d)
             self.y_perm, self.y = self._new(nr, d), self._new(self.T, d)
-        if not self.recompute and self.g is None:
+        if self.act8:
+            if self.g8 is None:
+                self.g8, self.u8 = self._rows8(nr, F), self._rows8(nr, F)
+                if self.shared_ff > 0:
+                    self.g8_s, self.u8_s = self._rows8(self.T, self.shared_ff), self._rows8(self.T, self.shared_ff)
+            if self.mxfp8 and self.mx.bf16_intermediates and self.h is None:
+                self.h = self._new(nr, F)
+        elif not self.recompute and self.g is None:
             self.g, self.u = self._new(nr, F), self._new(nr, F)
             if not (self.mxfp8 and not self.mx.bf16_intermediates):   # else H only as MXFP8 copies
                 self.h = self._new(nr, F)
         if self.mxfp8:   # the MXFP8 expert GEMMs write into the layer's buffers
             self.mx.g, self.mx.u, self.mx.h, self.mx.y_perm = self.g, self.u, self.h, self.y_perm
+            self.mx.g8, self.mx.u8 = self.g8, self.u8
 
     def backward_buffers(self):
         """Gradient buffers (kept across steps) and the backward's scratch."""
@@ -163,16 +189,23 @@ class MoELayer:
             mx.dg, mx.du, mx.dx_perm = self.dg, self.du, self.dx_perm
             mx.dw_gate, mx.dw_up, mx.dw_down = self.dw_gate, self.dw_up, self.dw_down
 
+    def _rows8(self, rows, cols):
+        """MXFP8 rows: codes [rows, cols] and a scale byte per 32 values."""
+        return L.MxTensor(self._new(rows, cols, dt=torch.uint8), self._new(rows * cols // 32, dt=torch.uint8))
+
     def _mark(self, name: str):
         if self.hook is not None:
             self.hook(name)
 
     # ------------------------------------------------------------------ helpers
-    def _gg(self, op, **tensors):
+    def _gg(self, op, ckpt=None, **tensors):
         grp = None if self.capacity > 0 else self.offsets
         desc = L.make_gg_desc(op, self._dt, self.E, self.d, self.F, self.n_rows, self.capacity,
                               grp, ws=self.ws_gg, **tensors)
-        L.moe_grouped_gemm(desc)
+        if ckpt is not None:
+            L.moe_grouped_gemm_ckpt(desc, *ckpt)
+        else:
+            L.moe_grouped_gemm(desc)
 
     # ------------------------------------------------------------------ passes
     def route(self, x, w_r):
@@ -181,12 +214,22 @@ class MoELayer:
         L.moe_route(self.logits, self.k, self.topk_idx, self.topk_w)
         self._mark("route")
 
-    def _gg_shared(self, op, **tensors):
+    def _gg_shared(self, op, ckpt=None, **tensors):
         desc = L.make_gg_desc(op, self._dt, 1, self.d, self.shared_ff, self.T, 0, self.offsets_s,
                               ws=self.ws_gg, **tensors)
-        L.moe_grouped_gemm(desc)
+        if ckpt is not None:
+            L.moe_grouped_gemm_ckpt(desc, *ckpt)
+        else:
+            L.moe_grouped_gemm(desc)
 
     def shared_forward(self):
+        if self.act8:
+            h = self._new(self.T, self.shared_ff)   # scratch for the down projection
+            self._gg_shared(L.MOE_GG_FWD_GATE_UP, ckpt=(self.g8_s, self.u8_s), x_perm=self.x, w_gate=self.w_gate_s,
+                            w_up=self.w_up_s, h=h)
+            self._gg_shared(L.MOE_GG_FWD_DOWN, h=h, w_down=self.w_down_s, y_perm=self.y_s)
+            self._mark("gg_shared_fwd")
+            return
         self._gg_shared(L.MOE_GG_FWD_GATE_UP, x_perm=self.x, w_gate=self.w_gate_s, w_up=self.w_up_s,
                         g=self.g_s, u=self.u_s, h=self.h_s)
         self._gg_shared(L.MOE_GG_FWD_DOWN, h=self.h_s, w_down=self.w_down_s, y_perm=self.y_s)
@@ -198,8 +241,13 @@ class MoELayer:
 
     def shared_backward_data(self, dy):
         """dG_s, dU_s and the shared expert's share of dx (dx_s)."""
-        self._gg_shared(L.MOE_GG_DGRAD_DOWN, dy_perm=dy, w_down=self.w_down_s, g=self.g_s, u=self.u_s,
-                        dg=self.dg_s, du=self.du_s)
+        if self.act8:
+            self.h_s = self._new(self.T, self.shared_ff)
+            self._gg_shared(L.MOE_GG_DGRAD_DOWN, ckpt=(self.g8_s, self.u8_s), dy_perm=dy, w_down=self.w_down_s,
+                            dg=self.dg_s, du=self.du_s, h=self.h_s)
+        else:
+            self._gg_shared(L.MOE_GG_DGRAD_DOWN, dy_perm=dy, w_down=self.w_down_s, g=self.g_s, u=self.u_s,
+                            dg=self.dg_s, du=self.du_s)
         self._gg_shared(L.MOE_GG_DGRAD_GATE_UP, dg=self.dg_s, du=self.du_s, w_gate=self.w_gate_s,
                         w_up=self.w_up_s, dx_perm=self.dx_s)
         self._mark("gg_shared_bwd_data")
@@ -209,15 +257,23 @@ class MoELayer:
         self._gg_shared(L.MOE_GG_WGRAD_GATE_UP, x_perm=self.x, dg=self.dg_s, du=self.du_s,
                         dw_gate=self.dw_gate_s, dw_up=self.dw_up_s)
         self._mark("gg_shared_bwd_weights")
+        if self.act8 and not self.keep_intermediates:
+            self.h_s = None
 
     def forward(self, x, w_gate, w_up, w_down, w_r=None, topk_idx=None, topk_w=None,
-                w_gate_s=None, w_up_s=None, w_down_s=None):
+                w_gate_s=None, w_up_s=None, w_down_s=None, x8=None):
+        """x8 (act8 only): the MXFP8 rows of x, as moe_add_rmsnorm writes them
+        beside x; without it they are quantised here."""
+        if x8 is not None and not self.act8:
+            raise ValueError("x8 is what a layer with act8 keeps of its input")
         self.x, self.w_gate, self.w_up, self.w_down, self.w_r = x, w_gate, w_up, w_down, w_r
         if self.shared_ff > 0:
             if w_gate_s is None or w_up_s is None or w_down_s is None:
                 raise ValueError("a layer with a shared expert needs its weights")
             self.w_gate_s, self.w_up_s, self.w_down_s = w_gate_s, w_up_s, w_down_s
         self.forward_buffers()
+        if self.act8:
+            self._keep_input(x, x8)
         if self.routing == "learned":
             self.route(x, w_r)
         else:
@@ -228,7 +284,34 @@ class MoELayer:
         if self.shared_ff > 0:
             self.shared_forward()
         self.combine()
+        if self.act8:   # the backward has the input's 8-bit rows
+            self.x = None
         return self.y
+
+    def _keep_input(self, x, x8):
+        """The input's 8-bit rows, where the backward reads the input (the
+        MXFP8 experts hold their own copy of the permuted rows)."""
+        if self.mxfp8 and self.routing != "learned":
+            return
+        if x8 is None:
+            if self.x8 is None:
+                self.x8 = self._rows8(self.T, self.d)
+            L.moe_mx_quantize(x, 0, self.x8.q, self.x8.s)
+            self._mark("quantize_x")
+            self._x8 = self.x8
+        else:
+            self._x8 = x8
+
+    def _restore_input(self):
+        """x and x_perm as the backward reads them, from the 8-bit rows."""
+        if not self.mxfp8:
+            self.x, self.x_perm = self._new(self.T, self.d), self._new(self.n_rows, self.d)
+            L.moe_permute_from_mx(self._x8, self.k, self.row_of, self.src_slot if self.capacity > 0 else None,
+                                  self.x_perm, x=self.x)
+        elif self.routing == "learned":
+            self.x = self._new(self.T, self.d)
+            L.moe_mx_dequantize(self._x8, self.x)
+        self._mark("restore_x")
 
     def metadata(self):
         L.moe_offsets(self.topk_idx, self.E, self.capacity, self.counts, self.offsets, self.row_of,
@@ -241,6 +324,8 @@ class MoELayer:
                              self.mx.xq.t, self.mx.x_c.t)
             self._mark("permute_mx")
             return
+        if self.act8:
+            self.x_perm = self._new(self.n_rows, self.d)   # scratch of the forward
         L.moe_permute(self.x, self.k, self.row_of, self.src_slot if self.capacity > 0 else None,
                       self.x_perm)
         self._mark("permute")
@@ -260,6 +345,15 @@ class MoELayer:
             self._gg(L.MOE_GG_FWD_DOWN, h=h, w_down=self.w_down, y_perm=self.y_perm)
             self._mark("gg_fwd_down")
             return
+        if self.act8:
+            h = self._new(self.n_rows, self.F)   # scratch for the down projection
+            self._gg(L.MOE_GG_FWD_GATE_UP, ckpt=(self.g8, self.u8), x_perm=self.x_perm, w_gate=self.w_gate,
+                     w_up=self.w_up, h=h)
+            self._mark("gg_fwd_gate_up")
+            self.x_perm = None
+            self._gg(L.MOE_GG_FWD_DOWN, h=h, w_down=self.w_down, y_perm=self.y_perm)
+            self._mark("gg_fwd_down")
+            return
         self._gg(L.MOE_GG_FWD_GATE_UP, x_perm=self.x_perm, w_gate=self.w_gate, w_up=self.w_up,
                  g=self.g, u=self.u, h=self.h)
         self._mark("gg_fwd_gate_up")
@@ -276,6 +370,8 @@ class MoELayer:
         parallel exchange, waits on, and each data-gradient GEMM reads what
         the one before it just wrote), weight gradients last."""
         self.backward_buffers()
+        if self.act8:
+            self._restore_input()
         # with src_slot the adjoint runs in row order (see moe_unpermute_combine_bwd)
         L.moe_unpermute_combine_bwd(dy, self.y_perm, self.topk_w, self.row_of, self.src_slot,
                                     self.dy_perm, self.dtopk_w)
@@ -298,6 +394,8 @@ class MoELayer:
         self.experts_backward_weights()
         if self.shared_ff > 0:
             self.shared_backward_weights(dy)
+        if self.act8:   # the restored input goes at once
+            self.x = self.x_perm = None
         if not self.keep_intermediates:
             self.release_intermediates()
         return self.dx
@@ -308,6 +406,7 @@ class MoELayer:
         allocates them again from torch's caching allocator."""
         self.x_perm = self.g = self.u = self.h = self.y_perm = self.y = None
         self.dy_perm = self.dg = self.du = self.dx_perm = None
+        self.x8 = self._x8 = self.g8 = self.u8 = self.g8_s = self.u8_s = None
 
     def experts_backward(self):
         self.experts_backward_data()
@@ -326,8 +425,13 @@ class MoELayer:
             self._gg(L.MOE_GG_FWD_GATE_UP, x_perm=self.x_perm, w_gate=self.w_gate, w_up=self.w_up,
                      g=self.g, u=self.u, h=self.h)
             self._mark("gg_recompute_gate_up")
-        self._gg(L.MOE_GG_DGRAD_DOWN, dy_perm=self.dy_perm, w_down=self.w_down, g=self.g, u=self.u,
-                 dg=self.dg, du=self.du)
+        if self.act8:
+            self.h = self._new(self.n_rows, self.F)
+            self._gg(L.MOE_GG_DGRAD_DOWN, ckpt=(self.g8, self.u8), dy_perm=self.dy_perm, w_down=self.w_down,
+                     dg=self.dg, du=self.du, h=self.h)
+        else:
+            self._gg(L.MOE_GG_DGRAD_DOWN, dy_perm=self.dy_perm, w_down=self.w_down, g=self.g, u=self.u,
+                     dg=self.dg, du=self.du)
         self._mark("gg_dgrad_down")
         self._gg(L.MOE_GG_DGRAD_GATE_UP, dg=self.dg, du=self.du, w_gate=self.w_gate, w_up=self.w_up,
                  dx_perm=self.dx_perm)
@@ -344,7 +448,7 @@ class MoELayer:
         self._gg(L.MOE_GG_WGRAD_GATE_UP, x_perm=self.x_perm, dg=self.dg, du=self.du,
                  dw_gate=self.dw_gate, dw_up=self.dw_up)
         self._mark("gg_wgrad_gate_up")
-        if self.recompute and not self.keep_intermediates:
+        if self.act8 or (self.recompute and not self.keep_intermediates):
             self.g = self.u = self.h = None   # the recomputed scratch goes at once
 
     def grads(self) -> Dict[str, torch.Tensor]:

@@ -90,6 +90,7 @@ class MxExperts:
         # bf16 results
         self.bf16_intermediates = bf16_intermediates
         self.h = self.dg = self.du = None
+        self.g8 = self.u8 = None   # G and U as MXFP8 rows, kept in place of bf16 g and u where the caller assigns them
         if outputs:
             self.g, self.u = bf(n, F), bf(n, F)
             self.y_perm = bf(n, d)
@@ -111,8 +112,15 @@ class MxExperts:
             self.hook(name)
 
     def _gg(self, op, **kw):
+        ckpt = self.g8 is not None and op in (L.MOE_GG_FWD_GATE_UP, L.MOE_GG_DGRAD_DOWN)
+        if ckpt:
+            for name in ("out0", "out1") if op == L.MOE_GG_FWD_GATE_UP else ("g", "u"):
+                kw[name] = None
         desc = L.make_mx_gg_desc(op, self.E, self.d, self.F, self.n, self.offsets, self.P, ws=self.ws, **kw)
-        L.moe_grouped_gemm_mx(desc)
+        if ckpt:
+            L.moe_grouped_gemm_mx_ckpt(desc, self.g8, self.u8)
+        else:
+            L.moe_grouped_gemm_mx(desc)
 
     # ------------------------------------------------------------------ steps
     def quantize_weights(self, w_gate, w_up, w_down, force: bool = False) -> bool:
