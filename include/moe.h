@@ -496,6 +496,63 @@ int moe_grouped_gemm_mx(const moe_mx_gg_desc* desc, hipStream_t stream);
 int moe_grouped_gemm_mx_ckpt(const moe_mx_gg_desc* desc, const moe_mx_tensor* g, const moe_mx_tensor* u,
                              hipStream_t stream);
 
+/* ----------------------------------------------------------------- 4-bit experts
+ * The serving form of the expert layer: weights in 4 bits, for single tokens,
+ * decode batches and short prompts. Reading, per the public OCP Microscaling
+ * Formats v1.0 specification (MXFP4): blocks of 32 consecutive values along
+ * the contraction share one E8M0 scale byte (value 2^(code-127)); elements are
+ * E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; codes 0..7, sign 8).
+ * For a block with largest magnitude amax, X = max(floor(log2 amax) - 2, -127)
+ * (X = -127 for an all-zero block) and each element is v * 2^-X rounded to
+ * nearest-even and saturated to +-6. Inputs are finite.
+ *
+ * moe_w4_quantize: bf16 w [n_mat, K, N] (K the contraction: w_gate and w_up
+ * [E,d,F], w_down [E,F,d] as they are) -> codes and scales, laid out once in
+ * the order moe_experts_w4 reads them. Per matrix:
+ *   q [N/16][K/128][4][16][16]: byte j of (tile, step, g, n) holds the codes
+ *     of column 16*tile + n, values 128*step + 32*g + 2j (low half) and + 2j+1;
+ *   s [N/16][ceil(K/512)][4][16][4]: byte i of (tile, chunk, g, n) is the scale
+ *     code of block 4*(4*chunk + i) + g of that column (0 past K).
+ * moe_w4_code_bytes and moe_w4_scale_bytes give one matrix's bytes.
+ *   K % 128 == 0, N % 16 == 0; w and q 16-byte aligned, s 4-byte aligned.
+ *
+ * moe_experts_w4: with slot (t,j) routed to expert e = topk_idx[t,j],
+ *   H[t,j] = silu(x[t] Wg[e]) * (x[t] Wu[e])   (binary32, rounded once to bf16)
+ *   y[t]   = y_add[t] + sum_j topk_w[t,j] * (H[t,j] Wd[e])
+ * binary32 sums (over K in a fixed order, then over j), y rounded once to
+ * bf16. Slots whose id is outside [0,E) add nothing (their weight is not
+ * read): a token with no other slot gets y_add or zero, so padding tokens may
+ * carry -1. The same expert may appear in several slots of a token.
+ *   x, y_add (may be NULL) and y [T,d] bf16; topk_idx [T,k] int32, topk_w
+ *   [T,k] binary32, as moe_route writes them; d and F multiples of 128;
+ *   T*k <= MOE_W4_MAX_SLOTS (longer prompts: the grouped GEMMs). y may be
+ *   y_add, but not x. ws: moe_experts_w4_workspace_bytes(T, k, d, F) bytes,
+ *   16-byte aligned; calls sharing one workspace must be ordered on one
+ *   stream. */
+#define MOE_W4_MAX_SLOTS 4096
+typedef struct moe_w4_tensor {
+  const void* q;   /* codes */
+  const void* s;   /* scales */
+} moe_w4_tensor;
+
+typedef struct moe_w4_desc {
+  int T, d, E, k, F;
+  const void* x;
+  const int32_t* topk_idx;
+  const float* topk_w;
+  moe_w4_tensor w_gate, w_up, w_down;
+  const void* y_add;
+  void* y;
+  void* ws;
+  size_t ws_bytes;
+} moe_w4_desc;
+
+size_t moe_w4_code_bytes(int K, int N);
+size_t moe_w4_scale_bytes(int K, int N);
+int moe_w4_quantize(const void* w, int n_mat, int K, int N, void* q, void* s, hipStream_t stream);
+size_t moe_experts_w4_workspace_bytes(int T, int k, int d, int F);
+int moe_experts_w4(const moe_w4_desc* desc, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_F32, MOE_BF16 = 0, 1
+MOE_MAX_NORM_D, MOE_W4_MAX_SLOTS = 12288, 4096
 (MOE_GG_FWD_GATE_UP, MOE_GG_FWD_DOWN, MOE_GG_DGRAD_DOWN, MOE_GG_DGRAD_GATE_UP,
  MOE_GG_WGRAD_DOWN, MOE_GG_WGRAD_GATE_UP) = range(6)
 
@@ -48,6 +49,15 @@ class moe_mx_gg_desc(C.Structure):
         ("ws", _vp), ("ws_bytes", _sz),
         ("qo0_rows", moe_mx_tensor), ("qo0_cols", moe_mx_tensor),
         ("qo1_rows", moe_mx_tensor), ("qo1_cols", moe_mx_tensor),
+    ]
+
+
+class moe_w4_desc(C.Structure):
+    _fields_ = [
+        ("T", _i), ("d", _i), ("E", _i), ("k", _i), ("F", _i),
+        ("x", _vp), ("topk_idx", _vp), ("topk_w", _vp),
+        ("w_gate_q", _vp), ("w_gate_s", _vp), ("w_up_q", _vp), ("w_up_s", _vp), ("w_down_q", _vp), ("w_down_s", _vp),
+        ("y_add", _vp), ("y", _vp), ("ws", _vp), ("ws_bytes", _sz),
     ]
 
 
@@ -83,6 +93,11 @@ SIGNATURES = {
     "moe_grouped_gemm_mx": (_i, [C.POINTER(moe_mx_gg_desc), _vp]),
     "moe_grouped_gemm_mx_ckpt": (_i, [C.POINTER(moe_mx_gg_desc), C.POINTER(moe_mx_tensor), C.POINTER(moe_mx_tensor),
                                       _vp]),
+    "moe_w4_code_bytes": (_sz, [_i, _i]),
+    "moe_w4_scale_bytes": (_sz, [_i, _i]),
+    "moe_w4_quantize": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_experts_w4_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "moe_experts_w4": (_i, [C.POINTER(moe_w4_desc), _vp]),
 }
 
 _lib: Optional[C.CDLL] = None
@@ -502,3 +517,61 @@ def moe_grouped_gemm_mx(desc: moe_mx_gg_desc, stream=None):
 
 def moe_grouped_gemm_mx_ckpt(desc: moe_mx_gg_desc, g: MxTensor, u: MxTensor, stream=None):
     _call("moe_grouped_gemm_mx_ckpt", C.byref(desc), *_ckpt(desc, g, u), _stream(stream))
+
+
+# ----------------------------------------------------------------- 4-bit experts
+class W4Tensor:
+    """n_mat matrices [K, N] as MXFP4: codes q and scales s (uint8 tensors) in
+    the layout of moe_w4_quantize."""
+
+    def __init__(self, q: torch.Tensor, s: torch.Tensor, n_mat: int, K: int, N: int):
+        self.q, self.s, self.n_mat, self.K, self.N = q, s, n_mat, K, N
+
+    @classmethod
+    def empty(cls, n_mat: int, K: int, N: int, device="cuda") -> "W4Tensor":
+        e = lambda n: torch.empty(n_mat * n, dtype=torch.uint8, device=device)
+        return cls(e(moe_w4_code_bytes(K, N)), e(moe_w4_scale_bytes(K, N)), n_mat, K, N)
+
+    def _addresses(self, name: str, shape):
+        if (self.n_mat, self.K, self.N) != shape:
+            raise MoEError(f"{name}: {(self.n_mat, self.K, self.N)}, expected {shape}")
+        n, u8 = self.n_mat, torch.uint8
+        return (_req(self.q, f"{name}.q", u8, min_numel=n * (self.K * self.N // 2)),
+                _req(self.s, f"{name}.s", u8, min_numel=n * (-(-self.K // 512) * self.N * 16)))
+
+
+def moe_w4_code_bytes(K: int, N: int) -> int:
+    return lib().moe_w4_code_bytes(K, N)
+
+
+def moe_w4_scale_bytes(K: int, N: int) -> int:
+    return lib().moe_w4_scale_bytes(K, N)
+
+
+def moe_w4_quantize(w, out: W4Tensor, stream=None):
+    M, K, N = w.shape
+    _same_device(w, out.q, out.s)
+    _call("moe_w4_quantize", _req(w, "w", torch.bfloat16, (M, K, N)), M, K, N, *out._addresses("out", (M, K, N)),
+          _stream(stream))
+
+
+def moe_experts_w4_workspace_bytes(T, k, d, F) -> int:
+    return lib().moe_experts_w4_workspace_bytes(T, k, d, F)
+
+
+def moe_experts_w4(x, topk_idx, topk_w, w_gate: W4Tensor, w_up: W4Tensor, w_down: W4Tensor, y, ws, y_add=None,
+                   stream=None):
+    T, d = x.shape
+    k, E, F = topk_idx.shape[1], w_gate.n_mat, w_gate.N
+    bf = torch.bfloat16
+    _same_device(x, topk_idx, topk_w, w_gate.q, w_gate.s, w_up.q, w_up.s, w_down.q, w_down.s, y, y_add, ws)
+    desc = moe_w4_desc(T, d, E, k, F)
+    _fill(desc, [((desc, n), v) for n, v in (
+        ("x", _req(x, "x", bf, (T, d))), ("topk_idx", _req(topk_idx, "topk_idx", torch.int32, (T, k))),
+        ("topk_w", _req(topk_w, "topk_w", torch.float32, (T, k))),
+        *zip(("w_gate_q", "w_gate_s"), w_gate._addresses("w_gate", (E, d, F))),
+        *zip(("w_up_q", "w_up_s"), w_up._addresses("w_up", (E, d, F))),
+        *zip(("w_down_q", "w_down_s"), w_down._addresses("w_down", (E, F, d))),
+        ("y_add", _req(y_add, "y_add", bf, (T, d), optional=True)), ("y", _req(y, "y", bf, (T, d))), ("ws", _p(ws)))])
+    desc.ws_bytes = _nbytes(ws)
+    _call("moe_experts_w4", C.byref(desc), _stream(stream))

@@ -1,0 +1,99 @@
+"""Refusals of the 4-bit experts, on the host, and the header's constants."""
+import ctypes as C
+import os
+import re
+
+import pytest
+import torch
+
+from routing_grouped_expert_router_amd import _lib as L
+from routing_grouped_expert_router_amd.decode import MoEDecoder
+
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
+FAKE = 0x1000
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moe.h")
+
+
+def test_constants_and_layout():
+    text = open(HEADER).read()
+    for name in ("MOE_MAX_NORM_D", "MOE_W4_MAX_SLOTS"):
+        assert int(re.search(rf"#define {name} (\d+)", text).group(1)) == getattr(L, name)
+    # five ints, three pointers, three (codes, scales) pairs, y_add, y, ws, ws_bytes
+    assert C.sizeof(L.moe_w4_desc) == 24 + 8 * (3 + 6 + 4)
+
+
+def test_sizes():
+    lib = L.lib()
+    assert lib.moe_w4_code_bytes(256, 48) == 256 * 24
+    assert lib.moe_w4_scale_bytes(512, 16) == 256 and lib.moe_w4_scale_bytes(640, 32) == 1024
+    assert lib.moe_w4_code_bytes(0, 16) == 0 and lib.moe_w4_scale_bytes(128, -1) == 0
+    assert lib.moe_experts_w4_workspace_bytes(0, 2, 128, 128) == 0
+    assert lib.moe_experts_w4_workspace_bytes(3, 2, 256, 128) == 6 * 128 * 2 + 6 * 256 * 4
+
+
+def test_quantize_argument_errors():
+    f = L.lib().moe_w4_quantize
+    assert f(FAKE, 2, 192, 64, FAKE, FAKE, None) == INVALID       # K % 128
+    assert f(FAKE, 2, 256, 40, FAKE, FAKE, None) == INVALID       # N % 16
+    assert f(FAKE, -1, 256, 64, FAKE, FAKE, None) == INVALID
+    assert f(None, 2, 256, 64, FAKE, FAKE, None) == INVALID
+    assert f(FAKE + 2, 2, 256, 64, FAKE, FAKE, None) == INVALID
+    assert f(FAKE, 2, 256, 64, FAKE + 8, FAKE, None) == INVALID
+    assert f(FAKE, 2, 256, 64, FAKE, FAKE + 2, None) == INVALID
+    assert f(None, 0, 256, 64, None, None, None) == 0
+
+
+def desc(**kw):
+    g = L.moe_w4_desc(4, 256, 8, 2, 384)
+    for n in ("x", "topk_idx", "topk_w", "w_gate_q", "w_gate_s", "w_up_q", "w_up_s", "w_down_q", "w_down_s", "y", "ws"):
+        setattr(g, n, FAKE)
+    g.ws_bytes = 1 << 30
+    for n, v in kw.items():
+        setattr(g, n, v)
+    return g
+
+
+def test_experts_argument_errors():
+    lib = L.lib()
+    call = lambda **kw: lib.moe_experts_w4(C.byref(desc(**kw)), None)
+    assert lib.moe_experts_w4(None, None) == INVALID
+    assert call(T=0) == 0 and call(T=0, x=None, ws=None) == 0
+    assert call(T=-1) == INVALID and call(k=0) == INVALID and call(E=0) == INVALID
+    assert call(d=192) == INVALID and call(F=64) == INVALID
+    assert call(E=1025) == UNSUPPORTED and call(k=17) == UNSUPPORTED
+    assert call(T=2049) == UNSUPPORTED                                 # 4098 slots
+    for n in ("x", "topk_idx", "topk_w", "y", "w_gate_q", "w_up_s", "w_down_q"):
+        assert call(**{n: None}) == INVALID
+    for n in ("x", "y", "y_add", "w_up_q"):
+        assert call(**{n: FAKE + 8}) == INVALID
+    assert call(topk_idx=FAKE + 2) == INVALID and call(w_gate_s=FAKE + 1) == INVALID
+    need = lib.moe_experts_w4_workspace_bytes(4, 2, 256, 384)
+    assert call(ws=None) == WORKSPACE and call(ws_bytes=need - 1) == WORKSPACE and call(ws=FAKE + 8) == WORKSPACE
+
+
+def test_binding_refuses_mismatched_tensors():
+    T, d, E, k, F = 3, 256, 4, 2, 128
+    bf = torch.bfloat16
+    x, y = torch.zeros(T, d, dtype=bf), torch.zeros(T, d, dtype=bf)
+    idx, p = torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k)
+    wg, wd = L.W4Tensor.empty(E, d, F, device="cpu"), L.W4Tensor.empty(E, F, d, device="cpu")
+    ws = torch.empty(L.moe_experts_w4_workspace_bytes(T, k, d, F), dtype=torch.uint8)
+    with pytest.raises(L.MoEError, match="device tensors"):
+        L.moe_experts_w4(x, idx, p, wg, wg, wd, y, ws)
+    with pytest.raises(L.MoEError, match="w_down"):
+        L.moe_experts_w4(x, idx, p, wg, wg, wg, y, ws)
+    with pytest.raises(L.MoEError, match="topk_idx: dtype"):
+        L.moe_experts_w4(x, idx.long(), p, wg, wg, wd, y, ws)
+    with pytest.raises(L.MoEError, match="topk_w: shape"):
+        L.moe_experts_w4(x, idx, p[:2], wg, wg, wd, y, ws)
+    with pytest.raises(L.MoEError, match="w_up.s"):
+        L.moe_experts_w4(x, idx, p, wg, L.W4Tensor(wg.q, wg.s[:-1], E, d, F), wd, y, ws)
+    with pytest.raises(L.MoEError, match="y: dtype"):
+        L.moe_experts_w4(x, idx, p, wg, wg, wd, y.float(), ws)
+    with pytest.raises(L.MoEError, match="w: shape|out"):
+        L.moe_w4_quantize(torch.zeros(E, d, F, dtype=bf), wd)
+
+
+def test_decoder_refuses_batches_past_the_slot_limit():
+    with pytest.raises(ValueError, match="4096"):
+        MoEDecoder(None, None, torch.empty(8, 128, 128), None, None, k=4, max_tokens=1025)
