@@ -154,9 +154,11 @@ def _p(t: Optional[torch.Tensor]):
 def _call(name: str, *args):
     """Call entry point `name` with marshalled arguments, raising MoEError for
     host tensors or a non-zero status."""
-    if any(a is _HOST for a in args):
+    if _HOST in args:
         raise MoEError(f"{name}: libmoe needs device tensors")
-    _check(getattr(lib(), name)(*args), name)
+    status = getattr(_lib or lib(), name)(*args)
+    if status != 0:
+        _check(status, name)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -182,31 +184,41 @@ def _req(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional: bool
         if optional:
             return None
         raise MoEError(f"{name} is required")
-    dts = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t.dtype not in dts:
-        raise MoEError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dts)}")
+    if t.dtype is not dtype:
+        dts = dtype if isinstance(dtype, tuple) else (dtype,)
+        if t.dtype not in dts:
+            raise MoEError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dts)}")
     if not t.is_contiguous():
         raise MoEError(f"{name}: must be contiguous (dense row-major)")
-    if isinstance(shape, int):
-        if t.numel() != shape:
-            raise MoEError(f"{name}: {t.numel()} elements, expected {shape}")
-    elif shape is not None:
-        if t.dim() != len(shape) or any(w >= 0 and w != v for w, v in zip(shape, t.shape)):
+    if shape is not None and t.shape != shape:   # equal at once in almost every call
+        if isinstance(shape, int):
+            if t.numel() != shape:
+                raise MoEError(f"{name}: {t.numel()} elements, expected {shape}")
+        elif t.dim() != len(shape) or any(w >= 0 and w != v for w, v in zip(shape, t.shape)):
             raise MoEError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)} (-1 = any)")
-    if t.numel() < min_numel:
+    if min_numel and t.numel() < min_numel:
         raise MoEError(f"{name}: {t.numel()} elements, at least {min_numel} needed")
-    return _p(t)
+    return t.data_ptr() if t.is_cuda else _HOST
 
 
 def _nbytes(ws: torch.Tensor) -> int:
     return ws.numel() * ws.element_size()
 
 
+_has_device = False
+
+
 def _stream(stream=None):
-    if stream is None and not torch.cuda.is_available():
-        return None   # no device: the call raises on its (host) tensors first
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """Handle of `stream`, by default the current device's current one."""
+    global _has_device
+    if stream is not None:
+        return stream.cuda_stream
+    if not _has_device:
+        if not torch.cuda.is_available():
+            return None   # no device: the call raises on its (host) tensors first
+        torch.cuda.init()
+        _has_device = True
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _same_device(*tensors):
@@ -214,12 +226,14 @@ def _same_device(*tensors):
     tensor on another one."""
     cur = None
     for t in tensors:
-        if t is None or not t.is_cuda:
+        if t is None:
             continue
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.device.index != cur:
-            raise MoEError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+        at = t.get_device()   # -1: host memory, which the call refuses by itself
+        if at >= 0 and at != cur:
+            if cur is None:
+                cur = torch._C._cuda_getDevice()
+            if at != cur:
+                raise MoEError(f"a tensor is on cuda:{at}, the current device is cuda:{cur}")
 
 
 def _fill(desc, fields):
@@ -535,9 +549,9 @@ class W4Tensor:
     def _addresses(self, name: str, shape):
         if (self.n_mat, self.K, self.N) != shape:
             raise MoEError(f"{name}: {(self.n_mat, self.K, self.N)}, expected {shape}")
-        n, u8 = self.n_mat, torch.uint8
-        return (_req(self.q, f"{name}.q", u8, min_numel=n * (self.K * self.N // 2)),
-                _req(self.s, f"{name}.s", u8, min_numel=n * (-(-self.K // 512) * self.N * 16)))
+        n, u8, q, s = self.n_mat, torch.uint8, self.q, self.s
+        return (_req(q, f"{name}.q", u8, min_numel=n * (self.K * self.N // 2)),
+                _req(s, f"{name}.s", u8, min_numel=n * (-(-self.K // 512) * self.N * 16)))
 
 
 def moe_w4_code_bytes(K: int, N: int) -> int:
@@ -565,13 +579,10 @@ def moe_experts_w4(x, topk_idx, topk_w, w_gate: W4Tensor, w_up: W4Tensor, w_down
     k, E, F = topk_idx.shape[1], w_gate.n_mat, w_gate.N
     bf = torch.bfloat16
     _same_device(x, topk_idx, topk_w, w_gate.q, w_gate.s, w_up.q, w_up.s, w_down.q, w_down.s, y, y_add, ws)
-    desc = moe_w4_desc(T, d, E, k, F)
-    _fill(desc, [((desc, n), v) for n, v in (
-        ("x", _req(x, "x", bf, (T, d))), ("topk_idx", _req(topk_idx, "topk_idx", torch.int32, (T, k))),
-        ("topk_w", _req(topk_w, "topk_w", torch.float32, (T, k))),
-        *zip(("w_gate_q", "w_gate_s"), w_gate._addresses("w_gate", (E, d, F))),
-        *zip(("w_up_q", "w_up_s"), w_up._addresses("w_up", (E, d, F))),
-        *zip(("w_down_q", "w_down_s"), w_down._addresses("w_down", (E, F, d))),
-        ("y_add", _req(y_add, "y_add", bf, (T, d), optional=True)), ("y", _req(y, "y", bf, (T, d))), ("ws", _p(ws)))])
-    desc.ws_bytes = _nbytes(ws)
-    _call("moe_experts_w4", C.byref(desc), _stream(stream))
+    fields = (_req(x, "x", bf, (T, d)), _req(topk_idx, "topk_idx", torch.int32, (T, k)),
+              _req(topk_w, "topk_w", torch.float32, (T, k)), *w_gate._addresses("w_gate", (E, d, F)),
+              *w_up._addresses("w_up", (E, d, F)), *w_down._addresses("w_down", (E, F, d)),
+              _req(y_add, "y_add", bf, (T, d), optional=True), _req(y, "y", bf, (T, d)), _p(ws))
+    if _HOST in fields:
+        raise MoEError("moe_experts_w4: libmoe needs device tensors")
+    _call("moe_experts_w4", C.byref(moe_w4_desc(T, d, E, k, F, *fields, _nbytes(ws))), _stream(stream))
