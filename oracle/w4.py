@@ -47,23 +47,24 @@ def w4_dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
 
 
 def experts(x, topk_idx, topk_w, w_gate, w_up, w_down, store, y_add=None):
-    """y of the serving form, token by token and slot by slot; also, for
-    derived error bounds, sum_j |w| sum_f |H| |Wd| with H's own error weights."""
+    """y of the serving form, expert by expert; also, for derived error bounds,
+    sum_j |w| sum_f |H| |Wd| and the same with H's own error weights."""
     T, d = x.shape
     E, _, F = w_gate.shape
     y = np.zeros((T, d)) if y_add is None else np.array(y_add, dtype=np.float64)
     mag, hmag = np.zeros((T, d)), np.zeros((T, d))
-    for t in range(T):
-        for j, e in enumerate(topk_idx[t]):
-            if e < 0 or e >= E:
-                continue
-            g, u = x[t] @ w_gate[e], x[t] @ w_up[e]
-            s = 1 / (1 + np.exp(-g))
-            h = store(g * s * u)
-            p = float(topk_w[t, j])
-            y[t] += p * (h @ w_down[e])
-            mag[t] += abs(p) * (np.abs(h) @ np.abs(w_down[e]))
-            # |dH| per unit of relative error of the sums behind g and u (|silu'| < 1.1)
-            ag, au = np.abs(x[t]) @ np.abs(w_gate[e]), np.abs(x[t]) @ np.abs(w_up[e])
-            hmag[t] += abs(p) * ((1.1 * ag * np.abs(u) + np.abs(g * s) * au) @ np.abs(w_down[e]))
+    topk_idx = np.asarray(topk_idx)
+    for e in range(E):
+        t, j = np.nonzero(topk_idx == e)
+        if not len(t):
+            continue
+        p, xe, ad = np.asarray(topk_w, dtype=np.float64)[t, j][:, None], x[t], np.abs(w_down[e])
+        g, u = xe @ w_gate[e], xe @ w_up[e]
+        s = 1 / (1 + np.exp(-g))
+        h = store(g * s * u)
+        np.add.at(y, t, p * (h @ w_down[e]))
+        np.add.at(mag, t, np.abs(p) * (np.abs(h) @ ad))
+        # |dH| per unit of relative error of the sums behind g and u (|silu'| < 1.1)
+        ag, au = np.abs(xe) @ np.abs(w_gate[e]), np.abs(xe) @ np.abs(w_up[e])
+        np.add.at(hmag, t, np.abs(p) * ((1.1 * ag * np.abs(u) + np.abs(g * s) * au) @ ad))
     return y, mag, hmag

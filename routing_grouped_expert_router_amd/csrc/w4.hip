@@ -23,11 +23,15 @@ namespace {
 
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 w4bf16x8_t;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float w4f32x4_t;
+typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t w4u32x4_t;
 
 constexpr int kTileN = 16;      // columns of a tile
 constexpr int kStepK = 128;     // K values of a step
 constexpr int kChunk = 4;       // steps that share a scale word
 constexpr int kW4Threads = 256;
+constexpr int kFewRows = 32;    // slots an expert, on average, up to which rows go 16 at a time
+constexpr long kStreamBytes = 100L << 20;
+constexpr int kW4SumSlots = 8, kW4SumParts = 4;   // w4_down_sum_kernel: slots, parts of K
 
 struct W4Mat {
   const uint8_t* q;
@@ -123,6 +127,14 @@ MOE_DEV bool gather_rows(const int32_t* __restrict__ idx, int R, int E, int u, u
   return true;
 }
 
+// 16 code bytes a lane. NT: past the caches, for launches that read more
+// weights than the last-level cache (256 MB) keeps for the next one.
+template <bool NT> MOE_DEV V16 load_codes(const uint8_t* q, size_t i) {
+  const w4u32x4_t* p = reinterpret_cast<const w4u32x4_t*>(q) + i;
+  if constexpr (NT) return __builtin_bit_cast(V16, __builtin_nontemporal_load(p));
+  else return __builtin_bit_cast(V16, *p);
+}
+
 // Eight bf16 values of one code word under scale byte `code`.
 MOE_DEV w4bf16x8_t decode_w4(uint32_t w, float scale) {
   V16 v;
@@ -134,52 +146,6 @@ MOE_DEV w4bf16x8_t decode_w4(uint32_t w, float scale) {
 }
 MOE_DEV float w4_scale(uint32_t word, int step) {
   return __uint_as_float((word >> (8 * step) & 0xffu) << 23 | 0x400000u);
-}
-
-// Sums of NM matrices' 16-column tile over the wave's chunks of K, for RB
-// blocks of 16 rows: acc[m][rb] holds, in lane (row r = lane % 16, g = lane / 16),
-// columns 4g..4g+3 of row r. `row[rb]` is the lane's source row.
-template <int NM, int RB>
-MOE_DEV void w4_sums(const W4Mat (&mat)[NM], size_t tile, int K, int part, int parts, const uint16_t* const (&row)[RB],
-                     w4f32x4_t (&acc)[NM][RB]) {
-  const int lane = threadIdx.x & 63;
-  const int steps = K / kStepK, chunks = (steps + kChunk - 1) / kChunk;
-#pragma unroll
-  for (int m = 0; m < NM; ++m)
-#pragma unroll
-    for (int r = 0; r < RB; ++r) acc[m][r] = w4f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int c = part; c < chunks; c += parts) {
-    uint32_t sw[NM];
-    V16 qv[NM][kChunk];
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      sw[m] = reinterpret_cast<const uint32_t*>(mat[m].s)[(tile * chunks + c) * 64 + lane];
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i)   // a step past K reads the last one and is not used
-        qv[m][i] = reinterpret_cast<const V16*>(mat[m].q)[(tile * steps + min(c * kChunk + i, steps - 1)) * 64 + lane];
-    }
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      if (c * kChunk + i >= steps) break;   // wave-uniform
-      V16 xv[RB][4];
-#pragma unroll
-      for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          xv[r][j] = reinterpret_cast<const V16*>(row[r])[(c * kChunk + i) * 16 + (lane >> 4) * 4 + j];
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const float scale = w4_scale(sw[m], i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const w4bf16x8_t a = decode_w4(qv[m][i].w[j], scale);
-#pragma unroll
-          for (int r = 0; r < RB; ++r)
-            acc[m][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(w4bf16x8_t, xv[r][j]), acc[m][r], 0, 0, 0);
-        }
-      }
-    }
-  }
 }
 
 struct W4Args {
@@ -194,93 +160,280 @@ struct W4Args {
   int T, d, E, k, F;
 };
 
-// WK waves share a tile's K, 4 / WK tiles per workgroup. Their sums meet in
-// LDS and are added in the order of the parts.
-template <bool GATE_UP, int WK, int RB>
-MOE_DEV void w4_tile(const W4Args& a, const Rows& rows, int r0, int tile, bool valid, const uint16_t* list, float* red) {
-  constexpr int NM = GATE_UP ? 2 : 1;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int part = wave % WK;
+// Four columns of slot s, tile `tile`: H from the gate and up sums, rounded
+// once to the type the next product's matrix cores take, or the slot's output.
+template <bool GATE_UP, int NM>
+MOE_DEV void w4_store(const W4Args& a, int s, int tile, const w4f32x4_t (&v)[NM]) {
+  const size_t o = (size_t)s * (GATE_UP ? a.F : a.d) + tile * kTileN + 4 * ((threadIdx.x & 63) >> 4);
+  if constexpr (GATE_UP) {
+    float hv[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) hv[r] = silu(v[0][r]) * v[1][r];
+    *reinterpret_cast<uint2*>(a.h + o) = make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
+  } else {
+    *reinterpret_cast<float4*>(a.part + o) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+  }
+}
+
+// Few rows an expert (a decode batch): one block of 16 rows at a time, whose
+// chunk of x stays in registers while the wave runs down TPW column tiles, the
+// next tile's codes in flight under the current one's products. WK waves share
+// K, so a workgroup covers 4 / WK groups of TPW tiles and its waves' sums meet
+// in LDS once.
+template <bool GATE_UP, int WK, int TPW, bool NT>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
+  constexpr int NM = GATE_UP ? 2 : 1, TN = 4 / WK;
+  __shared__ uint16_t list[MOE_W4_MAX_SLOTS];
+  __shared__ int count[4];
+  __shared__ __attribute__((aligned(16))) float4 red[WK > 1 ? 4 * TPW * NM * 64 : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave % WK, grp = wave / WK;
   const int K = GATE_UP ? a.d : a.F, N = GATE_UP ? a.F : a.d;
-  const uint16_t* src[RB];
+  const int tiles = N / kTileN, groups = (tiles + TN * TPW - 1) / (TN * TPW);
+  const int u = blockIdx.x / groups, tile0 = blockIdx.x % groups * TN * TPW + grp * TPW;
+  Rows rows;
+  if (!gather_rows(a.idx, a.T * a.k, a.E, u, list, count, rows)) return;
+  const int steps = K / kStepK, chunks = (steps + kChunk - 1) / kChunk;
+  const size_t t0 = (size_t)rows.e * tiles;
+  const W4Mat mat[2] = {GATE_UP ? a.wg : a.wd, a.wu};
+  for (int r0 = 0; r0 < rows.n; r0 += 16) {
+    const int s = list[min(r0 + (lane & 15), rows.n - 1)];   // a row past the last reads the last one
+    const V16* src = reinterpret_cast<const V16*>(GATE_UP ? a.x + (size_t)(s / a.k) * K : a.h + (size_t)s * K) + (lane >> 4) * 4;
+    w4f32x4_t acc[TPW][NM];
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {   // a row past the last reads the last one; its sums are not stored
-    const int s = list[min(r0 + 16 * r + (lane & 15), rows.n - 1)];
-    src[r] = GATE_UP ? a.x + (size_t)(s / a.k) * K : a.h + (size_t)s * K;
-  }
-  w4f32x4_t acc[NM][RB];
-  const size_t t = (size_t)rows.e * (N / kTileN) + tile;
-  if (valid) {
-    if constexpr (GATE_UP) {
-      const W4Mat mat[2] = {a.wg, a.wu};
-      w4_sums<2, RB>(mat, t, K, part, WK, src, acc);
-    } else {
-      const W4Mat mat[1] = {a.wd};
-      w4_sums<1, RB>(mat, t, K, part, WK, src, acc);
-    }
-  }
-  if constexpr (WK > 1) {
-    // parts 1.. leave their sums, part 0 adds them
-    __syncthreads();
-    float4* slot = reinterpret_cast<float4*>(red) + (size_t)(wave - wave / WK - 1) * NM * RB * 64 + lane;
-    if (valid && part > 0)
+    for (int i = 0; i < TPW; ++i)
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
+      for (int m = 0; m < NM; ++m) acc[i][m] = w4f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int c = part; c < chunks; c += WK) {
+      V16 qv[2][NM][kChunk];
+      uint32_t sw[2][NM];
+      auto fetch = [&](int i, V16 (&q)[NM][kChunk], uint32_t (&w)[NM]) {
+        const size_t t = t0 + min(tile0 + i, tiles - 1);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) slot[(m * RB + r) * 64] = __builtin_bit_cast(float4, acc[m][r]);
-    __syncthreads();
-    if (!valid || part > 0) return;
-    for (int p = 1; p < WK; ++p) {
-      const float4* from = reinterpret_cast<const float4*>(red) + (size_t)(wave + p - wave / WK - 1) * NM * RB * 64 + lane;
+        for (int m = 0; m < NM; ++m) {
+          w[m] = reinterpret_cast<const uint32_t*>(mat[m].s)[(t * chunks + c) * 64 + lane];
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const float4 v = from[(m * RB + r) * 64];
-          acc[m][r] += w4f32x4_t{v.x, v.y, v.z, v.w};
+          for (int b = 0; b < kChunk; ++b)   // a step past K reads the last one and is not used
+            q[m][b] = load_codes<NT>(mat[m].q, (t * steps + min(c * kChunk + b, steps - 1)) * 64 + lane);
         }
+      };
+      fetch(0, qv[0], sw[0]);
+      V16 xv[kChunk][4];
+#pragma unroll
+      for (int b = 0; b < kChunk; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xv[b][j] = src[min(c * kChunk + b, steps - 1) * 16 + j];
+      // every load of the first tile is issued before its first product
+#pragma unroll
+      for (int b = 0; b < kChunk; ++b) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) pin(qv[0][m][b]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pin(xv[b][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) {
+        if (i + 1 < TPW) fetch(i + 1, qv[(i + 1) & 1], sw[(i + 1) & 1]);
+#pragma unroll
+        for (int b = 0; b < kChunk; ++b) {
+          if (c * kChunk + b >= steps) break;   // wave-uniform
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            const float scale = w4_scale(sw[i & 1][m], b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode_w4(qv[i & 1][m][b].w[j], scale),
+                                                                  __builtin_bit_cast(w4bf16x8_t, xv[b][j]), acc[i][m], 0, 0, 0);
+          }
+        }
+      }
     }
-  } else if (!valid) {
-    return;
-  }
-  const int n = tile * kTileN + 4 * (lane >> 4);
+    const int at = r0 + (lane & 15);
+    auto store = [&](int i, const w4f32x4_t (&v)[NM]) {
+      if (at < rows.n && tile0 + i < tiles) w4_store<GATE_UP>(a, list[at], tile0 + i, v);
+    };
+    if constexpr (WK == 1) {
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const int at = r0 + 16 * r + (lane & 15);
-    if (at >= rows.n) continue;
-    const size_t o = (size_t)list[at] * N + n;
-    if constexpr (GATE_UP) {
-      float hv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) hv[i] = silu(acc[0][r][i]) * acc[1][r][i];
-      // H is rounded once, to the type the next product's matrix cores take
-      *reinterpret_cast<uint2*>(a.h + o) = make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
+      for (int i = 0; i < TPW; ++i) store(i, acc[i]);
     } else {
-      *reinterpret_cast<float4*>(a.part + o) = make_float4(acc[0][r][0], acc[0][r][1], acc[0][r][2], acc[0][r][3]);
+      if (r0 > 0) __syncthreads();   // the sums before are read
+      float4* mine = red + (size_t)wave * TPW * NM * 64 + lane;
+#pragma unroll
+      for (int i = 0; i < TPW; ++i)
+#pragma unroll
+        for (int m = 0; m < NM; ++m) mine[(i * NM + m) * 64] = __builtin_bit_cast(float4, acc[i][m]);
+      __syncthreads();
+      for (int i = part; i < TPW; i += WK) {   // the group's waves share its tiles; parts are added in order
+        w4f32x4_t v[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          v[m] = w4f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int p = 0; p < WK; ++p)
+            v[m] += __builtin_bit_cast(w4f32x4_t, red[((size_t)(grp * WK + p) * TPW * NM + i * NM + m) * 64 + lane]);
+        }
+        store(i, v);
+      }
     }
   }
 }
 
-// LDS: the slot list, then the parts' sums (up to 4 - 4 / WK waves of NM * RB
-// tiles of 1 KB).
-template <bool GATE_UP, int WK>
-__global__ void __launch_bounds__(kW4Threads) w4_kernel(W4Args a) {
-  constexpr int NM = GATE_UP ? 2 : 1, TN = 4 / WK, kManyRows = 4;
+// Many rows an expert (short prompts, small pools): 64 rows at a time, so that
+// a decoded weight serves four products. The rows' 128-value steps go through
+// two LDS buffers that the four waves share, each wave runs down its own
+// column tiles; rows of 256 bytes have their 16-byte chunks XOR-swizzled by
+// the row, which spreads the 16 rows of a fragment over the banks. Row blocks
+// are dealt to the workgroups of grid dimension y.
+constexpr int kManyRows = 64;
+template <bool GATE_UP>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
+  constexpr int NM = GATE_UP ? 2 : 1, NT = GATE_UP ? 2 : 4, RB = kManyRows / 16;   // matrices, tiles a wave, row blocks
   __shared__ uint16_t list[MOE_W4_MAX_SLOTS];
   __shared__ int count[4];
-  __shared__ __attribute__((aligned(16))) float red[WK > 1 ? (4 - TN) * NM * kManyRows * 256 : 4];
-  const int R = a.T * a.k, N = GATE_UP ? a.F : a.d;
-  const int tiles = N / kTileN, groups = (tiles + TN - 1) / TN;
-  const int u = blockIdx.x / groups, tile = blockIdx.x % groups * TN + (threadIdx.x >> 6) / WK;
+  __shared__ w4u32x4_t xs[2][kManyRows * 16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int K = GATE_UP ? a.d : a.F, N = GATE_UP ? a.F : a.d;
+  const int tiles = N / kTileN, groups = (tiles + 4 * NT - 1) / (4 * NT);
+  const int u = blockIdx.x / groups, tile0 = (blockIdx.x % groups * 4 + wave) * NT;
   Rows rows;
-  if (!gather_rows(a.idx, R, a.E, u, list, count, rows)) return;
-  const bool valid = tile < tiles;
-  const int tc = valid ? tile : tiles - 1;
-  if (rows.n <= 16) {
-    w4_tile<GATE_UP, WK, 1>(a, rows, 0, tc, valid, list, red);
-  } else {
-    for (int r0 = 0; r0 < rows.n; r0 += 16 * kManyRows)
-      w4_tile<GATE_UP, WK, kManyRows>(a, rows, r0, tc, valid, list, red);
+  if (!gather_rows(a.idx, a.T * a.k, a.E, u, list, count, rows)) return;
+  const int steps = K / kStepK, chunks = (steps + kChunk - 1) / kChunk;
+  const size_t t0 = (size_t)rows.e * tiles;
+  const W4Mat mat[2] = {GATE_UP ? a.wg : a.wd, a.wu};
+  const int sr = tid >> 4, sc = tid & 15;   // staging: rows sr + 16 i, chunk sc
+  for (int r0 = blockIdx.y * kManyRows; r0 < rows.n; r0 += gridDim.y * kManyRows) {
+    const w4u32x4_t* src[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {   // a row past the last reads the last one
+      const int s = list[min(r0 + sr + 16 * i, rows.n - 1)];
+      src[i] = reinterpret_cast<const w4u32x4_t*>(GATE_UP ? a.x + (size_t)(s / a.k) * K : a.h + (size_t)s * K) + sc;
+    }
+    w4u32x4_t xv[RB];
+    V16 qv[NM][NT];
+    uint32_t sw[NM][NT];
+    auto fetch = [&](int st) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) xv[i] = src[i][st * 16];
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const size_t t = t0 + min(tile0 + i, tiles - 1);
+          qv[m][i] = load_codes<false>(mat[m].q, (t * steps + st) * 64 + lane);
+          if (st % kChunk == 0) sw[m][i] = reinterpret_cast<const uint32_t*>(mat[m].s)[(t * chunks + st / kChunk) * 64 + lane];
+        }
+    };
+    w4f32x4_t acc[NM][NT][RB];
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[m][i][r] = w4f32x4_t{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();   // the block before is read
+    fetch(0);
+    for (int st = 0; st < steps; ++st) {
+      w4u32x4_t* buf = xs[st & 1];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) buf[(sr + 16 * i) * 16 + (sc ^ sr)] = xv[i];
+      V16 qc[NM][NT];
+      float scale[NM][NT];
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          qc[m][i] = qv[m][i];
+          scale[m][i] = w4_scale(sw[m][i], st % kChunk);
+        }
+      __syncthreads();   // one barrier a step: buffer st & 1 was last read at step st - 2
+      if (st + 1 < steps) fetch(st + 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w4bf16x8_t xf[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+          xf[r] = __builtin_bit_cast(w4bf16x8_t, buf[(16 * r + (lane & 15)) * 16 + (((lane >> 4) * 4 + j) ^ (lane & 15))]);
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const w4bf16x8_t w = decode_w4(qc[m][i].w[j], scale[m][i]);
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+              acc[m][i][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf[r], acc[m][i][r], 0, 0, 0);
+          }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int at = r0 + 16 * r + (lane & 15);
+      if (at >= rows.n) continue;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if (tile0 + i >= tiles) continue;
+        w4f32x4_t v[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) v[m] = acc[m][i][r];
+        w4_store<GATE_UP>(a, list[at], tile0 + i, v);
+      }
+    }
+  }
+}
+
+// The down product and the weighted sum at once, for a handful of slots: a
+// workgroup takes 16 output columns, its waves the (slot, chunk of K) pairs in
+// turn, every row of the product the same slot's H. A slot's sums over K are
+// added in order, then the token's slots.
+constexpr int kOneWaves = 8;
+__global__ void __launch_bounds__(64 * kOneWaves) w4_down_sum_kernel(W4Args a) {
+  __shared__ float red[kW4SumSlots * kW4SumParts][kTileN];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int R = a.T * a.k, steps = a.F / kStepK, chunks = (steps + kChunk - 1) / kChunk, tiles = a.d / kTileN;
+  const int parts = min(chunks, kW4SumParts);
+  for (int it = wave; it < R * parts; it += kOneWaves) {
+    const int s = it / parts, part = it % parts;
+    const int e = a.idx[s];
+    if (e < 0 || e >= a.E) continue;
+    const size_t t = (size_t)e * tiles + blockIdx.x;
+    const V16* src = reinterpret_cast<const V16*>(a.h + (size_t)s * a.F) + (lane >> 4) * 4;
+    w4f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c = part; c < chunks; c += parts) {
+      const uint32_t sw = reinterpret_cast<const uint32_t*>(a.wd.s)[(t * chunks + c) * 64 + lane];
+      V16 qv[kChunk], xv[kChunk][4];
+#pragma unroll
+      for (int b = 0; b < kChunk; ++b) {
+        const int st = min(c * kChunk + b, steps - 1);
+        qv[b] = reinterpret_cast<const V16*>(a.wd.q)[(t * steps + st) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xv[b][j] = src[st * 16 + j];
+      }
+#pragma unroll
+      for (int b = 0; b < kChunk; ++b) {
+        if (c * kChunk + b >= steps) break;   // wave-uniform
+        const float scale = w4_scale(sw, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode_w4(qv[b].w[j], scale), __builtin_bit_cast(w4bf16x8_t, xv[b][j]),
+                                                        acc, 0, 0, 0);
+      }
+    }
+    if ((lane & 15) == 0)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) red[it][4 * (lane >> 4) + r] = acc[r];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.T * kTileN; i += 64 * kOneWaves) {
+    const int t = i / kTileN, c = i % kTileN;
+    const size_t o = (size_t)t * a.d + blockIdx.x * kTileN + c;
+    float v = a.y_add ? bf16_to_f32(a.y_add[o]) : 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const int s = t * a.k + j, e = a.idx[s];
+      if (e < 0 || e >= a.E) continue;
+      float p = 0.f;
+      for (int q = 0; q < parts; ++q) p += red[s * parts + q][c];
+      v = fmaf(a.topk_w[s], p, v);
+    }
+    a.y[o] = f32_to_bf16(v);
   }
 }
 
@@ -298,30 +451,60 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(W4Args a) {
     v[2] = __uint_as_float(w.y << 16);
     v[3] = __uint_as_float(w.y & 0xffff0000u);
   }
-  for (int j = 0; j < a.k; ++j) {
-    const size_t s = (size_t)t * a.k + j;
-    const int e = a.idx[s];
-    if (e < 0 || e >= a.E) continue;
-    const float w = a.topk_w[s];
-    const float4 p = reinterpret_cast<const float4*>(a.part + s * a.d)[c];
-    v[0] = fmaf(w, p.x, v[0]);
-    v[1] = fmaf(w, p.y, v[1]);
-    v[2] = fmaf(w, p.z, v[2]);
-    v[3] = fmaf(w, p.w, v[3]);
+  constexpr int G = 4;   // slots whose loads are in flight together
+  for (int j0 = 0; j0 < a.k; j0 += G) {
+    int e[G];
+    float w[G];
+    float4 p[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {   // a slot past k reads the last one and adds nothing
+      const size_t s = (size_t)t * a.k + min(j0 + j, a.k - 1);
+      e[j] = j0 + j < a.k ? a.idx[s] : -1;
+      w[j] = a.topk_w[s];
+      p[j] = reinterpret_cast<const float4*>(a.part + s * a.d)[c];
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      if (e[j] < 0 || e[j] >= a.E) continue;
+      v[0] = fmaf(w[j], p[j].x, v[0]);
+      v[1] = fmaf(w[j], p[j].y, v[1]);
+      v[2] = fmaf(w[j], p[j].z, v[2]);
+      v[3] = fmaf(w[j], p[j].w, v[3]);
+    }
   }
   reinterpret_cast<uint2*>(a.y + (size_t)t * a.d)[c] = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
+template <bool GATE_UP, int WK, bool NT> void launch_few(const W4Args& a, long units, int tiles, hipStream_t s) {
+  constexpr int TN = 4 / WK;
+  // as many tiles a wave as leave four workgroups a CU
+  auto grid = [&](int tpw) { return units * ((tiles + TN * tpw - 1) / (TN * tpw)); };
+  if (grid(4) >= 1024) w4_few_kernel<GATE_UP, WK, 4, NT><<<(int)grid(4), kW4Threads, 0, s>>>(a);
+  else if (grid(2) >= 1024) w4_few_kernel<GATE_UP, WK, 2, NT><<<(int)grid(2), kW4Threads, 0, s>>>(a);
+  else w4_few_kernel<GATE_UP, WK, 1, NT><<<(int)grid(1), kW4Threads, 0, s>>>(a);
+}
+template <bool GATE_UP, bool NT> void launch_few(const W4Args& a, int wk, long units, int tiles, hipStream_t s) {
+  if (wk == 4) launch_few<GATE_UP, 4, NT>(a, units, tiles, s);
+  else if (wk == 2) launch_few<GATE_UP, 2, NT>(a, units, tiles, s);
+  else launch_few<GATE_UP, 1, NT>(a, units, tiles, s);
+}
+
 template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
-  const int K = GATE_UP ? a.d : a.F, N = GATE_UP ? a.F : a.d;
+  const int K = GATE_UP ? a.d : a.F, N = GATE_UP ? a.F : a.d, R = a.T * a.k, tiles = N / kTileN;
   const int chunks = (K / kStepK + kChunk - 1) / kChunk;
   const int wk = chunks >= 3 ? 4 : chunks;   // waves that share a tile's K: as many as it has chunks, up to 4
-  const int tn = 4 / wk;
-  const long units = min(a.T * a.k, a.E), grid = units * ((N / kTileN + tn - 1) / tn);
-  MOE_CHECK_SUPPORTED(grid < (1L << 31));
-  if (wk == 4) w4_kernel<GATE_UP, 4><<<(int)grid, kW4Threads, 0, s>>>(a);
-  else if (wk == 2) w4_kernel<GATE_UP, 2><<<(int)grid, kW4Threads, 0, s>>>(a);
-  else w4_kernel<GATE_UP, 1><<<(int)grid, kW4Threads, 0, s>>>(a);
+  const long units = min(R, a.E);
+  MOE_CHECK_SUPPORTED(units * tiles < (1L << 31));
+  if (R <= kFewRows * a.E) {
+    const long bytes = units * 3 * a.d * (long)a.F * 17 / 32;
+    if (bytes >= kStreamBytes) launch_few<GATE_UP, true>(a, wk, units, tiles, s);
+    else launch_few<GATE_UP, false>(a, wk, units, tiles, s);
+  } else {
+    constexpr int kCols = 4 * (GATE_UP ? 2 : 4);
+    const int groups = (tiles + kCols - 1) / kCols, blocks = (R + kManyRows - 1) / kManyRows;
+    const long want = (512 + units * groups - 1) / (units * groups);   // two workgroups a CU
+    w4_many_kernel<GATE_UP><<<dim3((unsigned)(units * groups), (unsigned)min((long)blocks, want)), kW4Threads, 0, s>>>(a);
+  }
   return launch_status();
 }
 
@@ -375,6 +558,10 @@ extern "C" int moe_experts_w4(const moe_w4_desc* g, hipStream_t stream) {
                  static_cast<const uint16_t*>(g->y_add), static_cast<uint16_t*>(g->y), reinterpret_cast<uint16_t*>(ws),
                  reinterpret_cast<float*>(ws + w4_part_offset(g->T, g->k, g->F)), g->T, g->d, g->E, g->k, g->F};
   if (int st = launch_w4<true>(a, stream)) return st;
+  if (g->T * g->k <= kW4SumSlots) {
+    w4_down_sum_kernel<<<g->d / kTileN, 64 * kOneWaves, 0, stream>>>(a);
+    return launch_status();
+  }
   if (int st = launch_w4<false>(a, stream)) return st;
   w4_combine_kernel<<<(int)(((long)g->T * (g->d / 4) + 255) / 256), 256, 0, stream>>>(a);
   return launch_status();
