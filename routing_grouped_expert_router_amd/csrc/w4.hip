@@ -29,9 +29,19 @@ constexpr int kTileN = 16;      // columns of a tile
 constexpr int kStepK = 128;     // K values of a step
 constexpr int kChunk = 4;       // steps that share a scale word
 constexpr int kW4Threads = 256;
-constexpr int kFewRows = 32;    // slots an expert, on average, up to which rows go 16 at a time
+// Slots an expert, on average, up to which rows go 16 at a time: the 64-row
+// kernel takes over where its workgroups fill the chip, later where they do
+// not. Measured (d 2048, F 1024, both kernels): 32 experts, 16 rows each,
+// 52 us against 42; 8 experts, 16 rows, 22 against 29; 32 rows, 32 against 30.
+constexpr int kFewRows = 12, kFewRowsSmall = 30;
+// Weight bytes of a launch from which the codes go past the caches (the
+// last-level one holds 256 MB): 167 MB 47 us against 43, 372 MB 78 against 72,
+// but 53 MB, which three weight sets in turn leave in it, 19 against 21.
 constexpr long kStreamBytes = 100L << 20;
-constexpr int kW4SumSlots = 8, kW4SumParts = 4;   // w4_down_sum_kernel: slots, parts of K
+// Slots up to which the down product and the weighted sum are one launch, and
+// its parts of K: 4 slots 9.6 us against 12.9 (both products), 8 slots 12.7
+// against 14.3, 16 slots 18.9 against 18.0.
+constexpr int kW4SumSlots = 8, kW4SumParts = 4;
 
 struct W4Mat {
   const uint8_t* q;
@@ -285,9 +295,10 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
 // the row, which spreads the 16 rows of a fragment over the banks. Row blocks
 // are dealt to the workgroups of grid dimension y.
 constexpr int kManyRows = 64;
+template <bool GATE_UP> constexpr int kManyTiles = GATE_UP ? 1 : 2;   // tiles a wave
 template <bool GATE_UP>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
-  constexpr int NM = GATE_UP ? 2 : 1, NT = GATE_UP ? 2 : 4, RB = kManyRows / 16;   // matrices, tiles a wave, row blocks
+  constexpr int NM = GATE_UP ? 2 : 1, NT = kManyTiles<GATE_UP>, RB = kManyRows / 16;   // matrices, tiles, row blocks
   __shared__ uint16_t list[MOE_W4_MAX_SLOTS];
   __shared__ int count[4];
   __shared__ w4u32x4_t xs[2][kManyRows * 16];
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
     }
     w4u32x4_t xv[RB];
     V16 qv[NM][NT];
-    uint32_t sw[NM][NT];
+    uint32_t sv[NM][NT];
     auto fetch = [&](int st) {
 #pragma unroll
       for (int i = 0; i < RB; ++i) xv[i] = src[i][st * 16];
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
         for (int i = 0; i < NT; ++i) {
           const size_t t = t0 + min(tile0 + i, tiles - 1);
           qv[m][i] = load_codes<false>(mat[m].q, (t * steps + st) * 64 + lane);
-          if (st % kChunk == 0) sw[m][i] = reinterpret_cast<const uint32_t*>(mat[m].s)[(t * chunks + st / kChunk) * 64 + lane];
+          sv[m][i] = mat[m].s[((t * chunks + st / kChunk) * 64 + lane) * kChunk + st % kChunk];
         }
     };
     w4f32x4_t acc[NM][NT][RB];
@@ -343,9 +354,9 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           qc[m][i] = qv[m][i];
-          scale[m][i] = w4_scale(sw[m][i], st % kChunk);
+          scale[m][i] = w4_scale(sv[m][i], 0);
         }
-      __syncthreads();   // one barrier a step: buffer st & 1 was last read at step st - 2
+      __syncthreads();   // one barrier a step: this buffer was last read two steps ago
       if (st + 1 < steps) fetch(st + 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -495,14 +506,15 @@ template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
   const int wk = chunks >= 3 ? 4 : chunks;   // waves that share a tile's K: as many as it has chunks, up to 4
   const long units = min(R, a.E);
   MOE_CHECK_SUPPORTED(units * tiles < (1L << 31));
-  if (R <= kFewRows * a.E) {
+  constexpr int kCols = 4 * kManyTiles<GATE_UP>;
+  const int groups = (tiles + kCols - 1) / kCols;
+  if (R <= (units * groups >= 512 ? kFewRows : kFewRowsSmall) * a.E) {
     const long bytes = units * 3 * a.d * (long)a.F * 17 / 32;
     if (bytes >= kStreamBytes) launch_few<GATE_UP, true>(a, wk, units, tiles, s);
     else launch_few<GATE_UP, false>(a, wk, units, tiles, s);
   } else {
-    constexpr int kCols = 4 * (GATE_UP ? 2 : 4);
-    const int groups = (tiles + kCols - 1) / kCols, blocks = (R + kManyRows - 1) / kManyRows;
-    const long want = (512 + units * groups - 1) / (units * groups);   // two workgroups a CU
+    const int blocks = (R + kManyRows - 1) / kManyRows;
+    const long want = (1024 + units * groups - 1) / (units * groups);   // four workgroups a CU
     w4_many_kernel<GATE_UP><<<dim3((unsigned)(units * groups), (unsigned)min((long)blocks, want)), kW4Threads, 0, s>>>(a);
   }
   return launch_status();
