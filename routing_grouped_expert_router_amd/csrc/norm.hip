@@ -11,17 +11,28 @@
 // contract of each entry point.
 #include "mx_common.h"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
 
-// 16-byte pieces of a row per lane: W waves hold rows of up to 256 W pieces.
-constexpr int kNormPieces = 4;
+// A row lies in the registers of W waves, U 16-byte pieces a lane. The smallest
+// of these that holds the row (16 waves of one workgroup would leave the
+// backward kernel 128 registers each, fewer than it needs, so 12 is the most):
+// pieces past the row are loaded and not used, so a tighter fit is faster
+// (4096 x 4096 bf16 backward: 35 us with W = 4, 33 with W = 2).
+template <typename T> constexpr int kNormMaxWaves = MOE_MAX_NORM_D / (64 * 4 * kVec<T>);   // 6 (bf16), 12 (binary32)
 
-// Waves per row: the fewest of 1, 4 and 6 (bf16) or 12 (binary32) that hold
-// the row, up to MOE_MAX_NORM_D (16 waves of one workgroup would leave the
-// backward kernel 128 registers each, fewer than it needs).
-template <typename T> constexpr int kNormMaxWaves = MOE_MAX_NORM_D / (64 * kNormPieces * kVec<T>);
+template <typename T, class F> void norm_shape(int d, F&& launch) {
+  const int per = 64 * kVec<T>;   // values a wave holds in one piece a lane
+  using std::integral_constant;
+  if (d <= 2 * per) launch(integral_constant<int, 1>(), integral_constant<int, 2>());
+  else if (d <= 4 * per) launch(integral_constant<int, 1>(), integral_constant<int, 4>());
+  else if (d <= 8 * per) launch(integral_constant<int, 2>(), integral_constant<int, 4>());
+  else if (d <= 16 * per) launch(integral_constant<int, 4>(), integral_constant<int, 4>());
+  else launch(integral_constant<int, kNormMaxWaves<T>>(), integral_constant<int, 4>());
+}
 
 struct NormArgs {
   const void* x;
@@ -38,11 +49,11 @@ struct NormArgs {
 
 // Piece c of a row: a wave-uniform base and a 32-bit byte offset, so that the
 // address costs one register.
-template <typename T> MOE_DEV V16 load_piece(const T* row, uint32_t c) {
-  return *reinterpret_cast<const V16*>(reinterpret_cast<const char*>(row) + c * 16u);
+template <bool NT, typename T> MOE_DEV V16 load_piece(const T* row, uint32_t c) {
+  return load16<NT>(reinterpret_cast<const char*>(row) + c * 16u);
 }
-template <typename T> MOE_DEV void store_piece(T* row, uint32_t c, const V16& v) {
-  *reinterpret_cast<V16*>(reinterpret_cast<char*>(row) + c * 16u) = v;
+template <bool NT, typename T> MOE_DEV void store_piece(T* row, uint32_t c, const V16& v) {
+  store16<NT>(reinterpret_cast<char*>(row) + c * 16u, v);
 }
 MOE_DEV uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
@@ -59,11 +70,15 @@ template <int W> MOE_DEV float row_sum(float v, float* red, int wave) {
   return t;
 }
 
-template <int W> constexpr int kNormThreads = W > 4 ? 64 * W : 256;
+template <int W> constexpr int kNormThreads = W == 1 ? 256 : 64 * W;   // four rows, or one
 
-template <typename T, int W, bool MX>
+// NT (launches that stream): x and res are read for the last time, h is next
+// read by the backward pass; y is read at once and goes through the caches.
+// Norm, router and permute of 16384 x 2048 rows: 137 us without, 112 us so,
+// 128 us with y past the caches too.
+template <typename T, int W, int U, bool MX, bool NT>
 __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a) {
-  constexpr int V = kVec<T>, U = kNormPieces;
+  constexpr int V = kVec<T>;
   __shared__ float red[W > 4 ? W : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const size_t t = W == 1 ? (size_t)blockIdx.x * 4 + wave : blockIdx.x;
@@ -76,13 +91,13 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
   const T* wp = static_cast<const T*>(a.w);
   V16 hv[U], rv[U], wv[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) hv[u] = load_piece(xp, umin(c0 + 64 * W * u, nvec - 1));
+  for (int u = 0; u < U; ++u) hv[u] = load_piece<NT>(xp, umin(c0 + 64 * W * u, nvec - 1));
   if (a.res) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) rv[u] = load_piece(rp, umin(c0 + 64 * W * u, nvec - 1));
+    for (int u = 0; u < U; ++u) rv[u] = load_piece<NT>(rp, umin(c0 + 64 * W * u, nvec - 1));
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) wv[u] = load_piece(wp, umin(c0 + 64 * W * u, nvec - 1));
+  for (int u = 0; u < U; ++u) wv[u] = load_piece<false>(wp, umin(c0 + 64 * W * u, nvec - 1));
   float ss = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -96,7 +111,7 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
       for (int i = 0; i < V; ++i) f[i] += r[i];
       hv[u] = pack(f);     // the norm is taken of h as it is stored
       unpack(hv[u], f);
-      if (in) store_piece(static_cast<T*>(a.h) + t * d, c0 + 64 * W * u, hv[u]);
+      if (in) store_piece<NT>(static_cast<T*>(a.h) + t * d, c0 + 64 * W * u, hv[u]);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) ss += in ? f[i] * f[i] : 0.f;
@@ -113,7 +128,7 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = f[i] * rs * w[i];
     const V16 yv = pack(f);
-    if (a.y && c < nvec) store_piece(static_cast<T*>(a.y) + t * d, c, yv);
+    if (a.y && c < nvec) store_piece<false>(static_cast<T*>(a.y) + t * d, c, yv);
     if constexpr (MX) {
       // four lanes hold a block of 32 values, sixteen the four blocks of a
       // scale word (nvec is a multiple of 16: no group straddles the row's end)
@@ -149,9 +164,9 @@ struct NormBwdArgs {
 };
 
 // Workgroups stride over the rows and keep their share of dw in registers.
-template <typename T, int W>
+template <typename T, int W, int U, bool NT>
 __global__ void __launch_bounds__(kNormThreads<W>) rmsnorm_bwd_kernel(NormBwdArgs a) {
-  constexpr int V = kVec<T>, U = kNormPieces, RPB = W == 1 ? 4 : 1;
+  constexpr int V = kVec<T>, RPB = W == 1 ? 4 : 1;
   __shared__ float red[2][W > 4 ? W : 4];
   __shared__ float sums[W == 1 ? 64 * U * V : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -162,7 +177,7 @@ __global__ void __launch_bounds__(kNormThreads<W>) rmsnorm_bwd_kernel(NormBwdArg
   float dw[U][V];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    wv[u] = load_piece(wp, umin(c0 + 64 * W * u, nvec - 1));
+    wv[u] = load_piece<false>(wp, umin(c0 + 64 * W * u, nvec - 1));
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[u][i] = 0.f;
   }
@@ -174,12 +189,12 @@ __global__ void __launch_bounds__(kNormThreads<W>) rmsnorm_bwd_kernel(NormBwdArg
     V16 gv[U], hv[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      gv[u] = load_piece(gp, umin(c0 + 64 * W * u, nvec - 1));
-      hv[u] = load_piece(hp, umin(c0 + 64 * W * u, nvec - 1));
+      gv[u] = load_piece<NT>(gp, umin(c0 + 64 * W * u, nvec - 1));
+      hv[u] = load_piece<NT>(hp, umin(c0 + 64 * W * u, nvec - 1));
     }
     if (a.dh) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) rv[u] = load_piece(rp, umin(c0 + 64 * W * u, nvec - 1));
+      for (int u = 0; u < U; ++u) rv[u] = load_piece<NT>(rp, umin(c0 + 64 * W * u, nvec - 1));
     }
     const float rs = a.rstd[t];
     float dot = 0.f;   // sum of g * n
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(kNormThreads<W>) rmsnorm_bwd_kernel(NormBwdArg
         const float v = rs * (g[i] * w[i] - (n[i] * rs) * mean);
         g[i] = a.dh ? r[i] + v : v;
       }
-      if (c < nvec) store_piece(static_cast<T*>(a.dx) + t * d, c, pack(g));
+      if (c < nvec) store_piece<false>(static_cast<T*>(a.dx) + t * d, c, pack(g));
     }
   }
   if (!a.part) return;
@@ -255,26 +270,36 @@ __global__ void __launch_bounds__(kNormThreads<W>) rmsnorm_bwd_kernel(NormBwdArg
   }
 }
 
-// dw[c] = sum over the parts, in a fixed order: 64 threads of a workgroup take
-// every 64th part of 4 columns each, then their sums are added in LDS.
-constexpr int kRedCols = 64;
+// dw[c] = sum over the parts, in a fixed order: 128 threads of a workgroup take
+// every 128th part of 4 columns each, four loads in flight, then their sums
+// are added in LDS. 32 columns a workgroup: 1024 parts of 2048 columns take
+// 3 us less than with 64.
+constexpr int kRedCols = 32, kRedRows = 1024 / (kRedCols / 4);
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int parts, int d,
                                                        T* __restrict__ dw) {
-  __shared__ float4 acc[64][kRedCols / 4];
-  const int ci = threadIdx.x & 15, gi = threadIdx.x >> 4;
+  constexpr int CL = kRedCols / 4, UN = 4;
+  __shared__ float4 acc[kRedRows][CL];
+  const int ci = threadIdx.x % CL, gi = threadIdx.x / CL;
   const int c = blockIdx.x * kRedCols + 4 * ci;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < d) {
-    for (int g = gi; g < parts; g += 64) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)g * d + c);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    for (int g = gi; g < parts; g += UN * kRedRows) {
+      float4 v[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u)   // a part past the last reads the last one and is left out
+        v[u] = *reinterpret_cast<const float4*>(part + (size_t)min(g + u * kRedRows, parts - 1) * d + c);
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        if (g + u * kRedRows >= parts) continue;
+        s.x += v[u].x; s.y += v[u].y; s.z += v[u].z; s.w += v[u].w;
+      }
     }
   }
   acc[gi][ci] = s;
   __syncthreads();
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
+  for (int o = kRedRows / 2; o > 0; o >>= 1) {
     if (gi < o) {
       const float4 v = acc[gi + o][ci];
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
@@ -290,36 +315,34 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   }
 }
 
-template <typename T> int norm_waves(int d) {
-  const int per = 64 * kNormPieces * kVec<T>;
-  return d <= per ? 1 : (d <= 4 * per ? 4 : kNormMaxWaves<T>);
-}
-
-// Workgroups of the backward kernel (and parts of dw).
-constexpr int kNormBwdGrid = 1024;
-int norm_bwd_grid(int T, int rows_per_block) {
-  const int blocks = (T + rows_per_block - 1) / rows_per_block;
-  return blocks < kNormBwdGrid ? blocks : kNormBwdGrid;
+// Workgroups of the backward kernel, and parts of dw: rows dealt evenly over
+// the workgroups that are resident at once (8 waves a CU in bf16, 12 in
+// binary32; 1024 at most). 16384 x 2048 bf16: 512 workgroups 48.4 us, 1024 50.7.
+template <typename T> int norm_bwd_grid(int T_, int waves) {
+  const int wg_waves = waves == 1 ? 4 : waves, rows = waves == 1 ? 4 : 1;
+  const int resident = min(256 * ((sizeof(T) == 2 ? 8 : 12) / wg_waves), 1024) * rows, per = (T_ + resident - 1) / resident;
+  return (T_ + per * rows - 1) / (per * rows);
 }
 
 template <typename T, bool MX> void launch_norm(const NormArgs& a, hipStream_t s) {
-  constexpr int M = kNormMaxWaves<T>;
-  switch (norm_waves<T>(a.d)) {
-    case 1: add_rmsnorm_kernel<T, 1, MX><<<(a.T + 3) / 4, 256, 0, s>>>(a); break;
-    case 4: add_rmsnorm_kernel<T, 4, MX><<<a.T, 256, 0, s>>>(a); break;
-    default: add_rmsnorm_kernel<T, M, MX><<<a.T, 64 * M, 0, s>>>(a);
-  }
+  const bool stream = (long)a.T * a.d * sizeof(T) * (a.res ? 4 : 2) >= kStreamBytes;
+  norm_shape<T>(a.d, [&](auto w, auto u) {
+    constexpr int W = w(), U = u();
+    const int grid = W == 1 ? (a.T + 3) / 4 : a.T;
+    if (stream) add_rmsnorm_kernel<T, W, U, MX, true><<<grid, kNormThreads<W>, 0, s>>>(a);
+    else add_rmsnorm_kernel<T, W, U, MX, false><<<grid, kNormThreads<W>, 0, s>>>(a);
+  });
 }
 
 template <typename T> int launch_norm_bwd(const NormBwdArgs& a, void* dw, hipStream_t s) {
-  constexpr int M = kNormMaxWaves<T>;
-  const int W = norm_waves<T>(a.d);
-  const int grid = norm_bwd_grid(a.T, W == 1 ? 4 : 1);
-  switch (W) {
-    case 1: rmsnorm_bwd_kernel<T, 1><<<grid, 256, 0, s>>>(a); break;
-    case 4: rmsnorm_bwd_kernel<T, 4><<<grid, 256, 0, s>>>(a); break;
-    default: rmsnorm_bwd_kernel<T, M><<<grid, 64 * M, 0, s>>>(a);
-  }
+  const bool stream = (long)a.T * a.d * sizeof(T) * (a.dh ? 4 : 3) >= kStreamBytes;
+  int grid = 0;
+  norm_shape<T>(a.d, [&](auto w, auto u) {
+    constexpr int W = w(), U = u();
+    grid = norm_bwd_grid<T>(a.T, W);
+    if (stream) rmsnorm_bwd_kernel<T, W, U, true><<<grid, kNormThreads<W>, 0, s>>>(a);
+    else rmsnorm_bwd_kernel<T, W, U, false><<<grid, kNormThreads<W>, 0, s>>>(a);
+  });
   if (int st = launch_status()) return st;
   if (!dw) return MOE_OK;
   norm_dw_kernel<T><<<(a.d + kRedCols - 1) / kRedCols, 1024, 0, s>>>(a.part, grid, a.d, static_cast<T*>(dw));
@@ -351,8 +374,8 @@ extern "C" int moe_add_rmsnorm(int dtype, const void* x, const void* res, const 
 
 extern "C" size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int d) {
   if (T < 1 || d < 1) return 0;
-  // parts of dw: one per workgroup, four rows or more each for short rows
-  return sizeof(float) * (size_t)norm_bwd_grid(T, 1) * d;
+  // one row of parts per workgroup, whatever the type: at most 1024, or T
+  return sizeof(float) * (size_t)min(T, 1024) * d;
 }
 
 extern "C" int moe_add_rmsnorm_bwd(int dtype, const void* dy, const void* h, const void* w, const float* rstd,

@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(const T* __restric
 // layout of T rows) and x_perm[row_of[t, j]] = the same; either output may be
 // null. Reads one byte and writes 2 (k + 1) per value, so the stores bound it:
 // eight values a lane keep each of them a whole 1 KB wave store.
+template <bool NT>
 __global__ void __launch_bounds__(kRowThreads) permute_from_mx_kernel(const uint8_t* __restrict__ q,
                                                                       const uint8_t* __restrict__ s, int T_, int d,
                                                                       int k, const int32_t* __restrict__ row_of,
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kRowThreads) permute_from_mx_kernel(const uint
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
       const int c = min(c0 + 64 * u, nvec - 1);
-      cq[u] = src[c];
+      cq[u] = load8<NT>(src + c);
       code[u] = s[4 * (static_cast<size_t>(T_) * (c >> 4) + t) + ((c >> 2) & 3)];
     }
     V16 v[kRowUnroll];
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kRowThreads) permute_from_mx_kernel(const uint
       V16* dst = reinterpret_cast<V16*>(j < 0 ? x + t * d : x_perm + (size_t)r * d);
 #pragma unroll
       for (int u = 0; u < kRowUnroll; ++u)
-        if (c0 + 64 * u < nvec) dst[c0 + 64 * u] = v[u];
+        if (c0 + 64 * u < nvec) store16<NT>(dst + c0 + 64 * u, v[u]);
     }
   }
 }
@@ -449,6 +450,15 @@ int zero_pads(const int32_t* src_slot, int n_rows, int d, void* buf, hipStream_t
   return launch_status();
 }
 
+int launch_from_mx(const void* q, const void* s, int T, int d, int k, const int32_t* row_of, int n_rows, void* x,
+                   void* x_perm, hipStream_t stream) {
+  auto* kernel = (long)T * d * (3 + 2 * k) >= kStreamBytes ? permute_from_mx_kernel<true> : permute_from_mx_kernel<false>;
+  kernel<<<row_grid(T), kRowThreads, 0, stream>>>(static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), T, d,
+                                                  k, row_of, n_rows, static_cast<uint16_t*>(x),
+                                                  static_cast<uint16_t*>(x_perm));
+  return launch_status();
+}
+
 }  // namespace
 
 extern "C" int moe_permute(int dtype, const void* x, int T, int d, int k, const int32_t* row_of,
@@ -480,20 +490,14 @@ extern "C" int moe_permute_from_mx(const void* q, const void* s, int T, int d, i
   if (src_slot)
     if (int st = zero_pads<uint16_t>(src_slot, n_rows, d, x_perm, stream)) return st;
   if (T == 0) return MOE_OK;
-  permute_from_mx_kernel<<<row_grid(T), kRowThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), T, d, k, row_of, n_rows,
-      static_cast<uint16_t*>(x), static_cast<uint16_t*>(x_perm));
-  return launch_status();
+  return launch_from_mx(q, s, T, d, k, row_of, n_rows, x, x_perm, stream);
 }
 
 extern "C" int moe_mx_dequantize(const void* q, const void* s, int rows, int cols, void* dst, hipStream_t stream) {
   MOE_CHECK_ARG(rows >= 0 && cols > 0 && cols % 128 == 0);
   if (rows == 0) return MOE_OK;
   MOE_CHECK_ARG(q && s && dst && aligned16(q) && aligned4(s) && aligned16(dst));
-  permute_from_mx_kernel<<<row_grid(rows), kRowThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), rows, cols, 0, nullptr, 0,
-      static_cast<uint16_t*>(dst), nullptr);
-  return launch_status();
+  return launch_from_mx(q, s, rows, cols, 0, nullptr, 0, dst, nullptr, stream);
 }
 
 extern "C" int moe_unpermute_combine(int dtype, const void* y_perm, const int32_t* row_of,

@@ -34,10 +34,6 @@ constexpr int kW4Threads = 256;
 // not. Measured (d 2048, F 1024, both kernels): 32 experts, 16 rows each,
 // 52 us against 42; 8 experts, 16 rows, 22 against 29; 32 rows, 32 against 30.
 constexpr int kFewRows = 12, kFewRowsSmall = 30;
-// Weight bytes of a launch from which the codes go past the caches (the
-// last-level one holds 256 MB): 167 MB 47 us against 43, 372 MB 78 against 72,
-// but 53 MB, which three weight sets in turn leave in it, 19 against 21.
-constexpr long kStreamBytes = 100L << 20;
 // Slots up to which the down product and the weighted sum are one launch, and
 // its parts of K: 4 slots 9.6 us against 12.9 (both products), 8 slots 12.7
 // against 14.3, 16 slots 18.9 against 18.0.
@@ -137,14 +133,6 @@ MOE_DEV bool gather_rows(const int32_t* __restrict__ idx, int R, int E, int u, u
   return true;
 }
 
-// 16 code bytes a lane. NT: past the caches, for launches that read more
-// weights than the last-level cache (256 MB) keeps for the next one.
-template <bool NT> MOE_DEV V16 load_codes(const uint8_t* q, size_t i) {
-  const w4u32x4_t* p = reinterpret_cast<const w4u32x4_t*>(q) + i;
-  if constexpr (NT) return __builtin_bit_cast(V16, __builtin_nontemporal_load(p));
-  else return __builtin_bit_cast(V16, *p);
-}
-
 // Eight bf16 values of one code word under scale byte `code`.
 MOE_DEV w4bf16x8_t decode_w4(uint32_t w, float scale) {
   V16 v;
@@ -224,7 +212,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
           w[m] = reinterpret_cast<const uint32_t*>(mat[m].s)[(t * chunks + c) * 64 + lane];
 #pragma unroll
           for (int b = 0; b < kChunk; ++b)   // a step past K reads the last one and is not used
-            q[m][b] = load_codes<NT>(mat[m].q, (t * steps + min(c * kChunk + b, steps - 1)) * 64 + lane);
+            q[m][b] = load16<NT>(mat[m].q + ((t * steps + min(c * kChunk + b, steps - 1)) * 64 + lane) * 16);
         }
       };
       fetch(0, qv[0], sw[0]);
@@ -330,7 +318,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const size_t t = t0 + min(tile0 + i, tiles - 1);
-          qv[m][i] = load_codes<false>(mat[m].q, (t * steps + st) * 64 + lane);
+          qv[m][i] = load16<false>(mat[m].q + ((t * steps + st) * 64 + lane) * 16);
           sv[m][i] = mat[m].s[((t * chunks + st / kChunk) * 64 + lane) * kChunk + st % kChunk];
         }
     };
@@ -510,6 +498,8 @@ template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
   const int groups = (tiles + kCols - 1) / kCols;
   if (R <= (units * groups >= 512 ? kFewRows : kFewRowsSmall) * a.E) {
     const long bytes = units * 3 * a.d * (long)a.F * 17 / 32;
+    // codes past the caches: 167 MB 47 us against 43, 372 MB 78 against 72, but
+    // 53 MB, which three weight sets in turn leave in them, 19 against 21
     if (bytes >= kStreamBytes) launch_few<GATE_UP, true>(a, wk, units, tiles, s);
     else launch_few<GATE_UP, false>(a, wk, units, tiles, s);
   } else {
