@@ -206,6 +206,7 @@ def _nbytes(ws: torch.Tensor) -> int:
 
 
 _has_device = False
+_one_device: Optional[bool] = None   # whether every device tensor is on the same device
 
 
 def _stream(stream=None):
@@ -224,6 +225,11 @@ def _stream(stream=None):
 def _same_device(*tensors):
     """The launches go to the current device's stream: raise for a device
     tensor on another one."""
+    global _one_device
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() <= 1
+    if _one_device:
+        return
     cur = None
     for t in tensors:
         if t is None:
@@ -276,15 +282,18 @@ def moe_route(logits, k, topk_idx, topk_w, stream=None):
 
 # ----------------------------------------------------------------- norm
 def moe_add_rmsnorm(x, w, eps, res=None, h=None, y=None, q: Optional[MxTensor] = None, rstd=None, stream=None):
-    T, d = x.shape
-    dt, u8 = x.dtype, torch.uint8
-    _same_device(x, w, res, h, y, rstd, *((q.q, q.s) if q is not None else ()))
-    _call("moe_add_rmsnorm", _dt(x), _req(x, "x", _FLOATS, (T, d)), _req(res, "res", dt, (T, d), optional=True),
-          _req(w, "w", dt, (d,)), T, d, eps, _req(h, "h", dt, (T, d), optional=True),
-          _req(y, "y", dt, (T, d), optional=True),
-          None if q is None else _req(q.q, "q.q", u8, min_numel=T * d),
-          None if q is None else _req(q.s, "q.s", u8, min_numel=T * d // 32),
-          _req(rstd, "rstd", torch.float32, (T,), optional=True), _stream(stream))
+    dt, shape = x.dtype, x.shape
+    T, d = shape
+    if q is None:
+        codes = scales = None
+        _same_device(x, w, res, h, y, rstd)
+    else:
+        codes = _req(q.q, "q.q", torch.uint8, min_numel=T * d)
+        scales = _req(q.s, "q.s", torch.uint8, min_numel=T * d // 32)
+        _same_device(x, w, res, h, y, rstd, q.q, q.s)
+    _call("moe_add_rmsnorm", _dt(x), _req(x, "x", dt, shape), _req(res, "res", dt, shape, True),
+          _req(w, "w", dt, (d,)), T, d, eps, _req(h, "h", dt, shape, True), _req(y, "y", dt, shape, True),
+          codes, scales, _req(rstd, "rstd", torch.float32, (T,), True), _stream(stream))
 
 
 def moe_add_rmsnorm_bwd_workspace_bytes(T, d) -> int:
@@ -295,7 +304,7 @@ def moe_add_rmsnorm_bwd(dy, h, w, rstd, dx, dw=None, dh=None, ws=None, stream=No
     T, d = dy.shape
     dt = dy.dtype
     _same_device(dy, h, w, rstd, dx, dw, dh, ws)
-    _call("moe_add_rmsnorm_bwd", _dt(dy), _req(dy, "dy", _FLOATS, (T, d)), _req(h, "h", dt, (T, d)),
+    _call("moe_add_rmsnorm_bwd", _dt(dy), _req(dy, "dy", dt, (T, d)), _req(h, "h", dt, (T, d)),
           _req(w, "w", dt, (d,)), _req(rstd, "rstd", torch.float32, (T,)), _req(dh, "dh", dt, (T, d), optional=True),
           T, d, _req(dx, "dx", dt, (T, d)), _req(dw, "dw", dt, (d,), optional=True), _p(ws),
           0 if ws is None else _nbytes(ws), _stream(stream))
@@ -549,9 +558,12 @@ class W4Tensor:
     def _addresses(self, name: str, shape):
         if (self.n_mat, self.K, self.N) != shape:
             raise MoEError(f"{name}: {(self.n_mat, self.K, self.N)}, expected {shape}")
-        n, u8, q, s = self.n_mat, torch.uint8, self.q, self.s
-        return (_req(q, f"{name}.q", u8, min_numel=n * (self.K * self.N // 2)),
-                _req(s, f"{name}.s", u8, min_numel=n * (-(-self.K // 512) * self.N * 16)))
+        M, K, N = shape
+        u8, q, s, nq, ns = torch.uint8, self.q, self.s, M * (K * N // 2), M * ((K + 511) // 512 * N * 16)
+        if (q.dtype is u8 and s.dtype is u8 and q.numel() >= nq and s.numel() >= ns and q.is_cuda and s.is_cuda
+                and q.is_contiguous() and s.is_contiguous()):
+            return q.data_ptr(), s.data_ptr()
+        return _req(q, f"{name}.q", u8, min_numel=nq), _req(s, f"{name}.s", u8, min_numel=ns)
 
 
 def moe_w4_code_bytes(K: int, N: int) -> int:
