@@ -101,8 +101,8 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float
  * bytes; both or neither NULL. y may be NULL when the copy is given. rstd [T]
  * binary32 (may be NULL) receives rs for the backward pass.
  *   x, res, h, y [T,d] and w [d] of `dtype`; d <= MOE_MAX_NORM_D; eps > 0.
- * h may be res or x itself and y may be x itself; other overlaps are not
- * allowed. Values whose squares overflow binary32 give rs = 0.
+ * h and y may each be x or res itself (not both the same one); other overlaps
+ * are not allowed. Values whose squares overflow binary32 give rs = 0.
  *
  * moe_add_rmsnorm_bwd: derived, its adjoint, with n = h * rs and g = dy * w:
  *   dx[t] = dh[t] + rs * (g - n * mean_i(g * n)), rounded once to `dtype`:

@@ -37,7 +37,7 @@ class MoEBlock:
 
     def forward(self, x, res, w_norm, *weights, **kw):
         """x and res [T, d] (res None: the first block, whose stream is x
-        itself); weights and the rest as MoELayer.forward takes them after x.
+        itself, which the backward reads again); weights and the rest as MoELayer.forward takes them after x.
         Returns (y, h)."""
         lay = self.layer
         if self.n is None:

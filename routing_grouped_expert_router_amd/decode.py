@@ -56,6 +56,8 @@ class MoEDecoder:
         T = x.shape[0]
         if T > self.T:
             raise ValueError(f"{T} tokens, made for {self.T}")
+        if T == 0:
+            return self.y[:0], x if res is None else self.h[:0]
         n, y, h = self.n[:T], self.y[:T], x if res is None else self.h[:T]
         L.moe_add_rmsnorm(x, self.w_norm, self.eps, res=res, h=None if res is None else h, y=n)
         logits, idx, p = self.logits[:T], self.topk_idx[:T], self.topk_w[:T]

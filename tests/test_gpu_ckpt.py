@@ -277,6 +277,56 @@ def test_block(opts, first):
     assert torch.equal(blk.backward(t["dy"], DH), first_dx)
 
 
+def test_two_blocks_against_autograd():
+    """A stack of two blocks in binary32 against automatic differentiation of
+    the definition in 64 bits: every gradient that a training step takes.
+    Sums of up to 160 terms, through four of them in turn: 1e-4 of the largest
+    element is 10^3 roundings of 2^-24."""
+    T, d, E, k, F = 33, 64, 4, 2, 160
+    g = torch.Generator().manual_seed(12)
+    rn = lambda *s, std=1.0: torch.randn(*s, generator=g) * std
+    x0 = rn(T, d)
+    par = [dict(w=1 + 0.1 * rn(d), wg=rn(E, d, F, std=d ** -0.5), wu=rn(E, d, F, std=d ** -0.5),
+                wd=rn(E, F, d, std=F ** -0.5),
+                idx=torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32),
+                p=torch.rand(T, k, generator=g)) for _ in range(2)]
+    dy, dh = rn(T, d), rn(T, d)
+    # the definition, differentiated
+    X = x0.double().requires_grad_()
+    P = [{n: (v if n == "idx" else v.double().requires_grad_()) for n, v in q.items()} for q in par]
+    x, res = X, None
+    for q in P:
+        h = x if res is None else x + res
+        n = h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6) * q["w"]
+        y = torch.zeros(T, d, dtype=torch.float64)
+        for j in range(k):
+            e = q["idx"][:, j].long()
+            a, b = (torch.einsum("td,tdf->tf", n, q[m][e]) for m in ("wg", "wu"))
+            y = y + q["p"][:, j:j + 1] * torch.einsum("tf,tfd->td", a * torch.sigmoid(a) * b, q["wd"][e])
+        x, res = y, h
+    ((x * dy).sum() + (res * dh).sum()).backward()
+    # the blocks
+    C = lambda v: v.detach().float().cuda() if v.dtype != torch.int32 else v.cuda()
+    blocks = [MoEBlock(T, d, E, k, F, torch.float32, routing="given") for _ in par]
+    cx, cres = C(x0), None
+    dev_par = [{n: C(v) for n, v in q.items()} for q in par]
+    for blk, q in zip(blocks, dev_par):
+        cx, cres = blk.forward(cx, cres, q["w"], q["wg"], q["wu"], q["wd"], topk_idx=q["idx"], topk_w=q["p"])
+    close = lambda got, ref, name: np.testing.assert_allclose(host(got), ref.detach().numpy(), rtol=0,
+                                                              atol=1e-4 * float(ref.detach().abs().max()), err_msg=name)
+    close(cx, x, "y")
+    close(cres, res, "h")
+    up, along = C(dy), C(dh)
+    for blk, q in list(zip(blocks, P))[::-1]:
+        dx = blk.backward(up, along)
+        grads = blk.layer.grads()
+        for name, ref in (("dw_gate", "wg"), ("dw_up", "wu"), ("dw_down", "wd"), ("dtopk_w", "p")):
+            close(grads[name], q[ref].grad, name)
+        close(blk.dw_norm, q["w"].grad, "dw_norm")
+        up = along = dx          # the sum's gradient is that of both of its terms
+    close(up, X.grad, "dx")
+
+
 def test_block_captured_and_replayed():
     """Forward and backward of a block in one graph, replayed beside eager runs
     of the same buffers' inputs."""

@@ -82,7 +82,7 @@ def check(y, ref, mag, hmag, K_d, K_F):
 
 
 CASES = [  # T, d, E, k, F: one token; slots up to the experts; more; rows past 16 and 64; K of 1 to 9 steps; one expert
-    (1, 256, 8, 2, 128), (1, 2048, 4, 4, 1024), (1, 128, 1, 1, 128), (3, 1152, 32, 4, 640), (2, 128, 4, 4, 512),
+    (1, 256, 8, 2, 128), (1, 2048, 4, 4, 1024), (1, 128, 1, 1, 128), (3, 1152, 12, 4, 640), (2, 128, 4, 4, 512),
     (16, 256, 4, 1, 256), (17, 256, 1, 1, 384), (70, 640, 3, 2, 128), (150, 128, 2, 2, 256), (9, 1024, 64, 8, 128),
     (64, 256, 128, 4, 128), (40, 384, 8, 8, 1152), (1, 4096, 2, 2, 128), (130, 1152, 3, 2, 384), (200, 256, 2, 2, 640),
 ]
@@ -224,6 +224,15 @@ def test_decode_step_captured_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(y, want[0]) and torch.equal(h, want[1]), i
         eager.step(res, x)                                       # other eager work between the replays
+
+
+def test_decode_step_of_no_tokens():
+    dec, _, _, _ = decoder(True)
+    e = torch.empty(0, 256, dtype=BF, device="cuda")
+    for out in (dec.step(e), dec.step(e, e)):
+        assert out[0].shape == out[1].shape == (0, 256)
+    with pytest.raises(ValueError, match="made for 20"):
+        dec.step(torch.empty(21, 256, dtype=BF, device="cuda"))
 
 
 def test_decode_on_another_stream():
