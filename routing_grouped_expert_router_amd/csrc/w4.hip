@@ -34,10 +34,20 @@ constexpr int kW4Threads = 256;
 // not. Measured (d 2048, F 1024, both kernels): 32 experts, 16 rows each,
 // 52 us against 42; 8 experts, 16 rows, 22 against 29; 32 rows, 32 against 30.
 constexpr int kFewRows = 12, kFewRowsSmall = 30;
-// Slots up to which the down product and the weighted sum are one launch, and
-// its parts of K: 4 slots 9.6 us against 12.9 (both products), 8 slots 12.7
-// against 14.3, 16 slots 18.9 against 18.0.
-constexpr int kW4SumSlots = 8, kW4SumParts = 4;
+// The down product and the weighted sum are one launch while few slots share
+// an expert's weights, which that launch reads once a slot: up to half the
+// experts, or up to two slots an expert where the caches keep the pool's down
+// weights; 64 slots at most. Both products, one launch against two: 4 slots of
+// 128 experts 9.7 us against 11.3, 16 slots 15.8 against 18.1, 64 slots 39.3
+// against 42.1, 128 slots 65 against 58; 64 slots of 32 experts with 36 MB of
+// down weights 28.2 against 28.4, with 143 MB 99 against 69; 8 experts, 32
+// slots, 14.7 against 14.1.
+inline bool sum_slots(int R, int E, long down_bytes) {
+  return R <= 64 && (2 * R <= E || (R <= 2 * E && down_bytes <= (40L << 20)));
+}
+// Slots a workgroup, and parts of K (16 slots in all: 15.8 us with 4 a
+// workgroup, 16.7 with 8).
+constexpr int kW4SumSlots = 4, kW4SumParts = 4;
 
 struct W4Mat {
   const uint8_t* q;
@@ -385,12 +395,13 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
 // added in order, then the token's slots.
 constexpr int kOneWaves = 8;
 __global__ void __launch_bounds__(64 * kOneWaves) w4_down_sum_kernel(W4Args a) {
-  __shared__ float red[kW4SumSlots * kW4SumParts][kTileN];
+  __shared__ float red[MOE_MAX_TOPK * kW4SumParts][kTileN];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int R = a.T * a.k, steps = a.F / kStepK, chunks = (steps + kChunk - 1) / kChunk, tiles = a.d / kTileN;
+  const int per = max(kW4SumSlots / a.k, 1), t0 = blockIdx.y * per, nt = min(per, a.T - t0);   // this workgroup's tokens
+  const int R = nt * a.k, steps = a.F / kStepK, chunks = (steps + kChunk - 1) / kChunk, tiles = a.d / kTileN;
   const int parts = min(chunks, kW4SumParts);
   for (int it = wave; it < R * parts; it += kOneWaves) {
-    const int s = it / parts, part = it % parts;
+    const int s = t0 * a.k + it / parts, part = it % parts;
     const int e = a.idx[s];
     if (e < 0 || e >= a.E) continue;
     const size_t t = (size_t)e * tiles + blockIdx.x;
@@ -421,15 +432,15 @@ __global__ void __launch_bounds__(64 * kOneWaves) w4_down_sum_kernel(W4Args a) {
       for (int r = 0; r < 4; ++r) red[it][4 * (lane >> 4) + r] = acc[r];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.T * kTileN; i += 64 * kOneWaves) {
+  for (int i = threadIdx.x; i < nt * kTileN; i += 64 * kOneWaves) {
     const int t = i / kTileN, c = i % kTileN;
-    const size_t o = (size_t)t * a.d + blockIdx.x * kTileN + c;
+    const size_t o = (size_t)(t0 + t) * a.d + blockIdx.x * kTileN + c;
     float v = a.y_add ? bf16_to_f32(a.y_add[o]) : 0.f;
     for (int j = 0; j < a.k; ++j) {
-      const int s = t * a.k + j, e = a.idx[s];
+      const int s = (t0 + t) * a.k + j, e = a.idx[s];
       if (e < 0 || e >= a.E) continue;
       float p = 0.f;
-      for (int q = 0; q < parts; ++q) p += red[s * parts + q][c];
+      for (int q = 0; q < parts; ++q) p += red[(t * a.k + j) * parts + q][c];
       v = fmaf(a.topk_w[s], p, v);
     }
     a.y[o] = f32_to_bf16(v);
@@ -560,8 +571,9 @@ extern "C" int moe_experts_w4(const moe_w4_desc* g, hipStream_t stream) {
                  static_cast<const uint16_t*>(g->y_add), static_cast<uint16_t*>(g->y), reinterpret_cast<uint16_t*>(ws),
                  reinterpret_cast<float*>(ws + w4_part_offset(g->T, g->k, g->F)), g->T, g->d, g->E, g->k, g->F};
   if (int st = launch_w4<true>(a, stream)) return st;
-  if (g->T * g->k <= kW4SumSlots) {
-    w4_down_sum_kernel<<<g->d / kTileN, 64 * kOneWaves, 0, stream>>>(a);
+  if (sum_slots(g->T * g->k, g->E, (long)g->E * g->d * g->F * 17 / 32)) {
+    const int per = g->k < kW4SumSlots ? kW4SumSlots / g->k : 1;
+    w4_down_sum_kernel<<<dim3(g->d / kTileN, (g->T + per - 1) / per), 64 * kOneWaves, 0, stream>>>(a);
     return launch_status();
   }
   if (int st = launch_w4<false>(a, stream)) return st;
