@@ -31,7 +31,7 @@ typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 dbf16x8_t;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short ds4_t;
 
 template <int BM_, int BN_, int WM_, int WN_, int BK_, int ST_, int OCC_ = 1> struct DmaCfg {
-  static constexpr bool kCkpt = false;
+  static constexpr bool kCkpt = false, kMxCopies = false;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, STAGES = ST_;
   static constexpr int OCC = OCC_;                         // workgroups per CU
   // waves per SIMD when OCC workgroups share a CU (HIP's second launch bound:

@@ -18,6 +18,13 @@ typedef __attribute__((__vector_size__(16 * sizeof(float)))) float df32x16_t;
 // division is a dozen instructions). Large |x| give exactly 0 or 1.
 MOE_DEV float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
+// dG and dU of one element from dH and the stored g and u.
+MOE_DEV void swiglu_bwd1(float dh, float g, float u, float& dg, float& du) {
+  const float sg = fast_sigmoid(g);
+  dg = dh * u * sg * (1.0f + g * (1.0f - sg));
+  du = dh * g * sg;
+}
+
 MOE_DEV uint2 dpack4(const float* v) { return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])); }
 MOE_DEV void dunpack4(uint2 p, float* v) {
   v[0] = __uint_as_float(p.x << 16);
@@ -247,28 +254,68 @@ MOE_DEV void gg_store_tile(const GGArgs& a, const df32x16_t (&acc)[C::MI][C::NI]
       store_plane(stg0, (uint16_t*)a.dw_gate + e * dF + rbase * F + n0, F, 0);
       store_plane(stg1, (uint16_t*)a.dw_up + e * dF + rbase * F + n0, F, 0);
     }
+  } else if constexpr (OP == MOE_GG_DGRAD_DOWN && C::kCkpt && !C::kMxCopies) {
+    // G and U from their 8-bit rows, and H from them again for the weight
+    // gradient. A pass takes the rows of one 32-row block of every wave (64
+    // rows of all BN columns), so that each wave works in both passes: with
+    // the passes over columns half of them idle, 2.4 us more where a tile or
+    // two is all a CU has.
+    static_assert(MI == 2 && C::WM == 2 && BM == 128 && 2 * (BM / 2) * (BN + 8) <= 2 * BM * LDW, "two planes of 64 rows");
+    constexpr int PR = BM / 2, LDP = BN + 8, CPRW = BN / 8;
+    uint16_t* pg = lds;
+    uint16_t* pu = lds + PR * LDP;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      auto tile_row = [&](int pr) { return (pr >> 5) * 64 + p * 32 + (pr & 31); };
+      for (int q = tid; q < PR * CPRW; q += NT) {
+        const int r = q / CPRW, c = q % CPRW, tr = tile_row(r);
+        if (tr >= rows_valid) continue;
+        const V16 gv = ckpt_get(a, 0, rbase + tr, n0 + c * 8);
+        const V16 uv = ckpt_get(a, 1, rbase + tr, n0 + c * 8);
+        *reinterpret_cast<V16*>(pg + r * LDP + c * 8) = gv;
+        *reinterpret_cast<V16*>(pu + r * LDP + c * 8) = uv;
+        if (a.h != nullptr) {
+          float gf[8], uf[8];
+          unpack(gv, gf);
+          unpack(uv, uf);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) gf[i] = gf[i] * uf[i] * fast_sigmoid(gf[i]);
+          *reinterpret_cast<V16*>((uint16_t*)a.h + (rbase + tr) * F + n0 + c * 8) = pack(gf);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int o = (wm * 32 + lr) * LDP + wcol0 + ni * 32 + 8 * g + 4 * lk;
+          float gf[4], uf[4], dg[4], du[4];
+          dunpack4(*reinterpret_cast<const uint2*>(pg + o), gf);
+          dunpack4(*reinterpret_cast<const uint2*>(pu + o), uf);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) swiglu_bwd1(acc[p][ni][4 * g + r], gf[r], uf[r], dg[r], du[r]);
+          *reinterpret_cast<uint2*>(pg + o) = dpack4(dg);
+          *reinterpret_cast<uint2*>(pu + o) = dpack4(du);
+        }
+      __syncthreads();
+      for (int q = tid; q < PR * CPRW; q += NT) {
+        const int r = q / CPRW, c = q % CPRW, tr = tile_row(r);
+        if (tr >= rows_valid) continue;
+        const size_t o = (rbase + tr) * F + n0 + c * 8;
+        *reinterpret_cast<V16*>((uint16_t*)a.dg + o) = *reinterpret_cast<const V16*>(pg + r * LDP + c * 8);
+        *reinterpret_cast<V16*>((uint16_t*)a.du + o) = *reinterpret_cast<const V16*>(pu + r * LDP + c * 8);
+      }
+      if (p == 0) __syncthreads();
+    }
   } else if (OP == MOE_GG_DGRAD_DOWN) {
     // per column chunk: stage G and U, turn them into dG and dU in place
     for (int ch = 0; ch < NCH; ++ch) {
-      if constexpr (C::kCkpt) {
-        // G and U from their 8-bit rows; H, wanted again by the weight
-        // gradient, from the same values
+      if constexpr (C::kCkpt) {   // from their 8-bit rows
         constexpr int CPRW = CW / 8;
-        uint16_t* outh = (uint16_t*)a.h + rbase * F + n0 + ch * CW;
         for (int q = tid; q < rows_valid * CPRW; q += NT) {
           const int r = q / CPRW, c = q % CPRW;
-          const V16 gv = ckpt_get(a, 0, rbase + r, n0 + ch * CW + c * 8);
-          const V16 uv = ckpt_get(a, 1, rbase + r, n0 + ch * CW + c * 8);
-          *reinterpret_cast<V16*>(stg0 + r * LDW + c * 8) = gv;
-          *reinterpret_cast<V16*>(stg1 + r * LDW + c * 8) = uv;
-          if (a.h != nullptr) {
-            float gf[8], uf[8];
-            unpack(gv, gf);
-            unpack(uv, uf);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) gf[i] = gf[i] * uf[i] * fast_sigmoid(gf[i]);
-            *reinterpret_cast<V16*>(outh + (size_t)r * F + c * 8) = pack(gf);
-          }
+          *reinterpret_cast<V16*>(stg0 + r * LDW + c * 8) = ckpt_get(a, 0, rbase + r, n0 + ch * CW + c * 8);
+          *reinterpret_cast<V16*>(stg1 + r * LDW + c * 8) = ckpt_get(a, 1, rbase + r, n0 + ch * CW + c * 8);
         }
       } else {
         load_plane(stg0, (const uint16_t*)a.g + rbase * F + n0, F, ch);
@@ -287,12 +334,7 @@ MOE_DEV void gg_store_tile(const GGArgs& a, const df32x16_t (&acc)[C::MI][C::NI]
               dunpack4(*reinterpret_cast<const uint2*>(stg0 + row * LDW + col), gf);
               dunpack4(*reinterpret_cast<const uint2*>(stg1 + row * LDW + col), uf);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float dh = acc[mi][ni][4 * g + r];
-                const float sg = fast_sigmoid(gf[r]);
-                dg[r] = dh * uf[r] * sg * (1.0f + gf[r] * (1.0f - sg));
-                du[r] = dh * gf[r] * sg;
-              }
+              for (int r = 0; r < 4; ++r) swiglu_bwd1(acc[mi][ni][4 * g + r], gf[r], uf[r], dg[r], du[r]);
               put4(stg0, row, col, dg);
               put4(stg1, row, col, du);
             }

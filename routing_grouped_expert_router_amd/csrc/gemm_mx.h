@@ -44,7 +44,7 @@ struct MxArgs {
 };
 
 template <int BM_, int BN_, int WM_, int WN_, int ST_, int OCC_> struct MxCfg {
-  static constexpr bool kCkpt = false;
+  static constexpr bool kCkpt = false, kMxCopies = true;   // the epilogue may write MXFP8 copies
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = ST_, OCC = OCC_;
   // waves per SIMD when OCC workgroups share a CU (HIP's second launch bound)
   static constexpr int WAVES_PER_SIMD = (WM_ * WN_ * OCC_ + 3) / 4;
