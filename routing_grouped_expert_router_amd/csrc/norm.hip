@@ -320,15 +320,16 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
 // binary32; 1024 at most). 16384 x 2048 bf16: 512 workgroups 48.4 us, 1024 50.7.
 template <typename T> int norm_bwd_grid(int T_, int waves) {
   const int wg_waves = waves == 1 ? 4 : waves, rows = waves == 1 ? 4 : 1;
-  const int resident = min(256 * ((sizeof(T) == 2 ? 8 : 12) / wg_waves), 1024) * rows, per = (T_ + resident - 1) / resident;
-  return (T_ + per * rows - 1) / (per * rows);
+  const long resident = min(256 * ((sizeof(T) == 2 ? 8 : 12) / wg_waves), 1024) * rows;
+  const long per = (T_ + resident - 1) / resident * rows;
+  return static_cast<int>((T_ + per - 1) / per);
 }
 
 template <typename T, bool MX> void launch_norm(const NormArgs& a, hipStream_t s) {
   const bool stream = (long)a.T * a.d * sizeof(T) * (a.res ? 4 : 2) >= kStreamBytes;
   norm_shape<T>(a.d, [&](auto w, auto u) {
     constexpr int W = w(), U = u();
-    const int grid = W == 1 ? (a.T + 3) / 4 : a.T;
+    const int grid = W == 1 ? static_cast<int>((a.T + 3L) / 4) : a.T;
     if (stream) add_rmsnorm_kernel<T, W, U, MX, true><<<grid, kNormThreads<W>, 0, s>>>(a);
     else add_rmsnorm_kernel<T, W, U, MX, false><<<grid, kNormThreads<W>, 0, s>>>(a);
   });

@@ -263,7 +263,8 @@ class MoELayer:
     def forward(self, x, w_gate, w_up, w_down, w_r=None, topk_idx=None, topk_w=None,
                 w_gate_s=None, w_up_s=None, w_down_s=None, x8=None):
         """x8 (act8 only): the MXFP8 rows of x, as moe_add_rmsnorm writes them
-        beside x; without it they are quantised here."""
+        beside x, which the backward reads again; without it they are
+        quantised here."""
         if x8 is not None and not self.act8:
             raise ValueError("x8 is what a layer with act8 keeps of its input")
         self.x, self.w_gate, self.w_up, self.w_down, self.w_r = x, w_gate, w_up, w_down, w_r

@@ -155,6 +155,40 @@ def test_backward(T, d, kind, with_dh):
         assert torch.equal(DH, first)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows of a long batch are those of the
+    same rows alone, forward (with the MXFP8 copy), backward and restore."""
+    d, n = 8192, 512
+    T = (1 << 31) // d + n
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rn = lambda: torch.randn(n, d, generator=g, device="cuda").to(torch.bfloat16)
+    w = (1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16)
+    small = [rn() for _ in range(3)]                              # x, res, dy
+
+    def run(x, res, dy):
+        m = x.shape[0]
+        h, y, dx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        q = L.MxTensor(torch.empty(m, d, dtype=torch.uint8, device="cuda"),
+                       torch.empty(m * d // 32, dtype=torch.uint8, device="cuda"))
+        rstd = torch.empty(m, device="cuda")
+        L.moe_add_rmsnorm(x, w, EPS, res=res, h=h, y=y, q=q, rstd=rstd)
+        L.moe_add_rmsnorm_bwd(dy, h, w, rstd, dx, dh=res)
+        back, perm = torch.empty_like(x), torch.empty_like(x)
+        L.moe_permute_from_mx(q, 1, torch.arange(m - 1, -1, -1, dtype=torch.int32, device="cuda"), None, perm, x=back)
+        return [v[-n:].clone() for v in (h, y, dx, q.q, back)] + [perm[:n].flip(0).clone()]
+
+    want = run(*small)
+    long = []
+    for v in small:
+        t = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+        t[-n:] = v
+        long.append(t)
+    got = run(*long)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(want[4], want[5]) and torch.equal(got[4], got[5])
+
+
 def test_backward_without_rows():
     dw = torch.full((264,), 7.0, dtype=torch.bfloat16, device="cuda")
     e = torch.empty(0, 264, dtype=torch.bfloat16, device="cuda")

@@ -160,6 +160,47 @@ def test_largest_batch():
     check(host(y), ref, mag, hmag, d, F)
 
 
+@pytest.mark.parametrize("T,d,E,k,F", [(4096, 128, 1, 1, 128), (256, 128, 1000, 16, 128), (1, 128, 1024, 16, 128)])
+def test_limits(T, d, E, k, F):
+    """Every slot on one expert, and the most experts and slots a token."""
+    x, idx, p, ws, _ = problem(T, d, E, k, F, 7)
+    w4 = [quantize_experts(bf(w)) for w in ws]
+    vals = [w4_dequantize(*w4_quantize(w)) for w in ws]
+    ref, mag, hmag = experts(x, idx, p, *vals, lambda a: a)
+    y = torch.empty(T, d, dtype=BF, device="cuda")
+    buf = torch.empty(L.moe_experts_w4_workspace_bytes(T, k, d, F), dtype=torch.uint8, device="cuda")
+    L.moe_experts_w4(bf(x), dev(idx, "i32"), dev(p, "f32"), *w4, y, buf)
+    check(host(y), ref, mag, hmag, d, F)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 4 GB of codes: its last experts give what they give
+    in a pool of their own."""
+    E, d, F, k, T = 1024, 2048, 4096, 2, 3
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rnd = lambda n: torch.randint(0, 256, (n,), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(T, d, generator=g, device="cuda").to(BF)
+    idx = torch.tensor([[1023, 1], [1022, 1023], [0, 1021]], dtype=torch.int32, device="cuda")
+    p = torch.rand(T, k, generator=g, device="cuda")
+    used, at = torch.unique(idx.view(-1).long(), return_inverse=True)
+    big, small = [], []
+    for K, N in ((d, F), (d, F), (F, d)):
+        nq, ns = L.moe_w4_code_bytes(K, N), L.moe_w4_scale_bytes(K, N)
+        q = torch.zeros(E, nq, dtype=torch.uint8, device="cuda")
+        q[used] = rnd(len(used) * nq).view(len(used), nq)
+        s = torch.full((E, ns), 119, dtype=torch.uint8, device="cuda")
+        assert E * nq > 1 << 31
+        big.append(L.W4Tensor(q.view(-1), s.view(-1), E, K, N))
+        small.append(L.W4Tensor(q[used].contiguous().view(-1), s[used].contiguous().view(-1), len(used), K, N))
+    out = []
+    for w4, i in ((big, idx), (small, at.view(T, k).to(torch.int32))):
+        y = torch.empty(T, d, dtype=BF, device="cuda")
+        buf = torch.empty(L.moe_experts_w4_workspace_bytes(T, k, d, F), dtype=torch.uint8, device="cuda")
+        L.moe_experts_w4(x, i, p, *w4, y, buf)
+        out.append(y)
+    assert bool(out[0].isfinite().all()) and bool((out[0] != 0).any()) and torch.equal(out[0], out[1])
+
+
 # ----------------------------------------------------------------------------- decode step
 def decoder(shared, max_tokens=20):
     g = np.random.default_rng(6)
