@@ -80,11 +80,12 @@ template <typename T, int W, int U, bool MX, bool NT>
 __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a) {
   constexpr int V = kVec<T>;
   __shared__ float red[W > 4 ? W : 4];
+  __shared__ uint32_t words[MX && W == 1 ? 4 * U : 1][4];   // scale words of four rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const size_t t = W == 1 ? (size_t)blockIdx.x * 4 + wave : blockIdx.x;
-  if (t >= (size_t)a.T) return;   // W == 1 only: no barrier follows there
+  // a wave past the last row works on it again and stores nothing
+  const size_t t1 = W == 1 ? (size_t)blockIdx.x * 4 + wave : blockIdx.x, t = t1 < (size_t)a.T ? t1 : a.T - 1;
   const int d = a.d;
-  const uint32_t nvec = d / V, c0 = (W == 1 ? 0 : wave * 64) + lane;
+  const uint32_t nvec = d / V, nst = t1 == t ? nvec : 0, c0 = (W == 1 ? 0 : wave * 64) + lane;
   // all loads first, unconditional: a piece past the row reads its last one
   const T* xp = static_cast<const T*>(a.x) + t * d;
   const T* rp = static_cast<const T*>(a.res ? a.res : a.x) + t * d;
@@ -111,14 +112,14 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
       for (int i = 0; i < V; ++i) f[i] += r[i];
       hv[u] = pack(f);     // the norm is taken of h as it is stored
       unpack(hv[u], f);
-      if (in) store_piece<NT>(static_cast<T*>(a.h) + t * d, c0 + 64 * W * u, hv[u]);
+      if (c0 + 64 * W * u < nst) store_piece<NT>(static_cast<T*>(a.h) + t * d, c0 + 64 * W * u, hv[u]);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) ss += in ? f[i] * f[i] : 0.f;
   }
   ss = row_sum<W>(ss, red, wave);
   const float rs = 1.0f / sqrtf(ss / (float)d + a.eps);
-  if (a.rstd && c0 == 0) a.rstd[t] = rs;
+  if (a.rstd && c0 < min(nst, 1u)) a.rstd[t] = rs;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t c = c0 + 64 * W * u;
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = f[i] * rs * w[i];
     const V16 yv = pack(f);
-    if (a.y && c < nvec) store_piece<false>(static_cast<T*>(a.y) + t * d, c, yv);
+    if (a.y && c < nst) store_piece<false>(static_cast<T*>(a.y) + t * d, c, yv);
     if constexpr (MX) {
       // four lanes hold a block of 32 values, sixteen the four blocks of a
       // scale word (nvec is a multiple of 16: no group straddles the row's end)
@@ -142,14 +143,29 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
       const uint32_t code = static_cast<uint32_t>(bs.x + 127);
       const uint32_t word = code | __shfl_down(code, 4, 64) << 8 | __shfl_down(code, 8, 64) << 16 |
                             __shfl_down(code, 12, 64) << 24;
-      if (c < nvec) {
+      if (c < nst) {
         reinterpret_cast<uint2*>(a.q + t * d)[c] = o;
-        if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(a.s + 4 * (static_cast<size_t>(a.T) * (c >> 4) + t)) = word;
+        if constexpr (W > 1) {
+          if ((lane & 15) == 0)
+            *reinterpret_cast<uint32_t*>(a.s + 4 * (static_cast<size_t>(a.T) * (c >> 4) + t)) = word;
+        }
+      }
+      if constexpr (W == 1) {
+        if ((lane & 15) == 0) words[4 * u + (lane >> 4)][wave] = word;
       }
     }
   }
+  if constexpr (MX && W == 1) {
+    // the four rows' words of a column group are neighbours: one store of
+    // 16-byte runs for all of them (52.8 us with a store a word, 50.9 so)
+    __syncthreads();
+    const uint32_t c = threadIdx.x >> 2;
+    const size_t row = (size_t)blockIdx.x * 4 + (threadIdx.x & 3);
+    if (c < nvec / 16 && row < (size_t)a.T)
+      *reinterpret_cast<uint32_t*>(a.s + 4 * (static_cast<size_t>(a.T) * c + row)) = words[c][threadIdx.x & 3];
+  }
 }
+
 
 // ------------------------------------------------------------------ backward
 struct NormBwdArgs {
