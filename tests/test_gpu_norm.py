@@ -3,8 +3,8 @@ float64 oracle.
 
 Tolerances. A stored value is off by at most half a step, S = 2^-8 (bf16) or
 2^-24 (binary32) of it. Sums of a row add at most 32 terms in a lane, then 6
-butterfly steps and 12 waves: 50 roundings, so a mean of squares is within
-50 * 2^-24 of itself, rs within half of that and four roundings more.
+butterfly steps and 12 waves: 50 roundings at most, so a mean of squares is
+within 50 * 2^-24 of itself, rs within half of that and a few roundings more.
 """
 import numpy as np
 import pytest
