@@ -154,9 +154,12 @@ def _p(t: Optional[torch.Tensor]):
 def _call(name: str, *args):
     """Call entry point `name` with marshalled arguments, raising MoEError for
     host tensors or a non-zero status."""
-    if _HOST in args:
-        raise MoEError(f"{name}: libmoe needs device tensors")
-    status = getattr(_lib or lib(), name)(*args)
+    try:
+        status = getattr(_lib or lib(), name)(*args)
+    except C.ArgumentError:   # the stand-in for a host tensor is no address
+        if any(a is _HOST for a in args):
+            raise MoEError(f"{name}: libmoe needs device tensors") from None
+        raise
     if status != 0:
         _check(status, name)
 
@@ -595,6 +598,10 @@ def moe_experts_w4(x, topk_idx, topk_w, w_gate: W4Tensor, w_up: W4Tensor, w_down
               _req(topk_w, "topk_w", torch.float32, (T, k)), *w_gate._addresses("w_gate", (E, d, F)),
               *w_up._addresses("w_up", (E, d, F)), *w_down._addresses("w_down", (E, F, d)),
               _req(y_add, "y_add", bf, (T, d), optional=True), _req(y, "y", bf, (T, d)), _p(ws))
-    if _HOST in fields:
-        raise MoEError("moe_experts_w4: libmoe needs device tensors")
-    _call("moe_experts_w4", C.byref(moe_w4_desc(T, d, E, k, F, *fields, _nbytes(ws))), _stream(stream))
+    try:
+        desc = moe_w4_desc(T, d, E, k, F, *fields, _nbytes(ws))
+    except TypeError:   # the stand-in for a host tensor is no address
+        if any(f is _HOST for f in fields):
+            raise MoEError("moe_experts_w4: libmoe needs device tensors") from None
+        raise
+    _call("moe_experts_w4", C.byref(desc), _stream(stream))
