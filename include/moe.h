@@ -517,7 +517,8 @@ int moe_grouped_gemm_mx_ckpt(const moe_mx_gg_desc* desc, const moe_mx_tensor* g,
  *   K % 128 == 0, N % 16 == 0; w and q 16-byte aligned, s 4-byte aligned.
  *
  * moe_experts_w4: with slot (t,j) routed to expert e = topk_idx[t,j],
- *   H[t,j] = silu(x[t] Wg[e]) * (x[t] Wu[e])   (binary32, rounded once to bf16)
+ *   H[t,j] = silu(x[t] Wg[e]) * (x[t] Wu[e])   (binary32, carried as two bf16
+ *                                               terms: within 2^-16 of itself)
  *   y[t]   = y_add[t] + sum_j topk_w[t,j] * (H[t,j] Wd[e])
  * binary32 sums (over K in a fixed order, then over j), y rounded once to
  * bf16. Slots whose id is outside [0,E) add nothing (their weight is not

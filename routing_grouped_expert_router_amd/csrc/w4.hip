@@ -31,8 +31,12 @@ constexpr int kChunk = 4;       // steps that share a scale word
 constexpr int kW4Threads = 256;
 // Slots an expert, on average, up to which rows go 16 at a time: the 64-row
 // kernel takes over where its workgroups fill the chip, later where they do
-// not. Measured (d 2048, F 1024, both kernels): 32 experts, 16 rows each,
-// 52 us against 42; 8 experts, 16 rows, 22 against 29; 32 rows, 32 against 30.
+// not, and for the down product, whose two terms make it 8 rows at a time, at
+// half as many. Measured (d 2048, F 1024, the call's time with 16 or 8 at a time
+// against 64): gate/up, 32 experts, 10 slots each, 42 us against 47, 16 slots 52
+// against 49; 8 experts, 16 slots, 27 against 31, 32 slots 31.3 against 30.9.
+// Down, 32 experts, 6 slots, 35 against 39, 8 slots 41 against 39; 8 experts,
+// 10 slots, 20 against 22, 16 slots 26.8 against 26.2, 20 slots 30 against 27.
 constexpr int kFewRows = 12, kFewRowsSmall = 30;
 // The down product and the weighted sum are one launch while few slots share
 // an expert's weights, which that launch reads once a slot: up to half the
@@ -163,28 +167,56 @@ struct W4Args {
   W4Mat wg, wu, wd;
   const uint16_t* y_add;   // [T, d] or null
   uint16_t* y;             // [T, d]
-  uint16_t* h;             // [R, F] workspace
+  uint16_t* h;             // [R, 2, F] workspace: each slot's hidden row in two terms
   float* part;             // [R, d] workspace: each slot's output row
   int T, d, E, k, F;
 };
 
-// Four columns of slot s, tile `tile`: H from the gate and up sums, rounded
-// once to the type the next product's matrix cores take, or the slot's output.
+// Rows of the products' second operand: x as it is, H as two bf16 terms, the
+// rounded value and what the rounding left (16 bits of H in all). One term
+// alone, as the training layer's H is, would put its 2^-8 beside y's own (2.4e-3
+// against 1.7e-3 relative). Up to eight rows the second term costs nothing: it
+// takes the places of the sixteen that those rows leave.
+template <bool GATE_UP> constexpr int kTerms = GATE_UP ? 1 : 2;
+template <bool GATE_UP, typename V> MOE_DEV const V* w4_row(const W4Args& a, int s) {
+  return reinterpret_cast<const V*>(GATE_UP ? a.x + (size_t)(s / a.k) * a.d : a.h + (size_t)s * 2 * a.F);
+}
+
+// A row's sums over H's two terms: lane i of sixteen has row i's first term,
+// lane 8 + i its second.
+MOE_DEV w4f32x4_t add_terms(w4f32x4_t v) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] += __shfl_xor(v[r], 8, 64);
+  return v;
+}
+
+// Four columns of slot s, tile `tile`: H's two terms from the gate and up
+// sums, or the slot's output.
 template <bool GATE_UP, int NM>
 MOE_DEV void w4_store(const W4Args& a, int s, int tile, const w4f32x4_t (&v)[NM]) {
-  const size_t o = (size_t)s * (GATE_UP ? a.F : a.d) + tile * kTileN + 4 * ((threadIdx.x & 63) >> 4);
+  const int col = tile * kTileN + 4 * ((threadIdx.x & 63) >> 4);
   if constexpr (GATE_UP) {
-    float hv[4];
+    float hv[4], lo[4];
+    uint32_t hi[2];
 #pragma unroll
     for (int r = 0; r < 4; ++r) hv[r] = silu(v[0][r]) * v[1][r];
-    *reinterpret_cast<uint2*>(a.h + o) = make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = pack_bf16x2(hv[2 * i], hv[2 * i + 1]);
+      const float a0 = __uint_as_float(hi[i] << 16), a1 = __uint_as_float(hi[i] & 0xffff0000u);
+      lo[2 * i] = __builtin_isfinite(a0) ? hv[2 * i] - a0 : 0.f;
+      lo[2 * i + 1] = __builtin_isfinite(a1) ? hv[2 * i + 1] - a1 : 0.f;
+    }
+    uint16_t* row = a.h + (size_t)s * 2 * a.F + col;
+    *reinterpret_cast<uint2*>(row) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(row + a.F) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
   } else {
-    *reinterpret_cast<float4*>(a.part + o) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+    *reinterpret_cast<float4*>(a.part + (size_t)s * a.d + col) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
   }
 }
 
 // Few rows an expert (a decode batch). 64 tokens, top-4 of 128 experts of
-// 2048 x 1024: gate/up 43 us at 6.0 TB/s, down 23 us at 5.7, the weights' bytes
+// 2048 x 1024: gate/up 44 us at 5.9 TB/s, down 26 us at 5.1, the weights' bytes
 // and little else. One block of 16 rows at a time, whose chunk of x stays in
 // registers while the wave runs down TPW column tiles, the next tile's codes
 // in flight under the current one's products (that batch: 72 us with four
@@ -192,7 +224,7 @@ MOE_DEV void w4_store(const W4Args& a, int s, int tile, const w4f32x4_t (&v)[NM]
 // covers 4 / WK groups of TPW tiles and its waves' sums meet in LDS once.
 template <bool GATE_UP, int WK, int TPW, bool NT>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
-  constexpr int NM = GATE_UP ? 2 : 1, TN = 4 / WK;
+  constexpr int NM = GATE_UP ? 2 : 1, TN = 4 / WK, NR = 16 / kTerms<GATE_UP>;   // rows at a time
   __shared__ uint16_t list[MOE_W4_MAX_SLOTS];
   __shared__ int count[4];
   __shared__ __attribute__((aligned(16))) float4 red[WK > 1 ? 4 * TPW * NM * 64 : 1];
@@ -206,9 +238,10 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
   const int steps = K / kStepK, chunks = (steps + kChunk - 1) / kChunk;
   const size_t t0 = (size_t)rows.e * tiles;
   const W4Mat mat[2] = {GATE_UP ? a.wg : a.wd, a.wu};
-  for (int r0 = 0; r0 < rows.n; r0 += 16) {
-    const int s = list[min(r0 + (lane & 15), rows.n - 1)];   // a row past the last reads the last one
-    const V16* src = reinterpret_cast<const V16*>(GATE_UP ? a.x + (size_t)(s / a.k) * K : a.h + (size_t)s * K) + (lane >> 4) * 4;
+  for (int r0 = 0; r0 < rows.n; r0 += NR) {
+    // a row past the last reads the last one; place NR + i of H's holds the second term of row i
+    const int s = list[min(r0 + (lane & (NR - 1)), rows.n - 1)];
+    const V16* src = w4_row<GATE_UP, V16>(a, s) + (lane >> 4) * 4 + (lane & 15) / NR * (K / 8);
     w4f32x4_t acc[TPW][NM];
 #pragma unroll
     for (int i = 0; i < TPW; ++i)
@@ -259,8 +292,9 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
       }
     }
     const int at = r0 + (lane & 15);
-    auto store = [&](int i, const w4f32x4_t (&v)[NM]) {
-      if (at < rows.n && tile0 + i < tiles) w4_store<GATE_UP>(a, list[at], tile0 + i, v);
+    auto store = [&](int i, w4f32x4_t (&v)[NM]) {
+      if constexpr (!GATE_UP) v[0] = add_terms(v[0]);
+      if ((lane & 15) < NR && at < rows.n && tile0 + i < tiles) w4_store<GATE_UP>(a, list[at], tile0 + i, v);
     };
     if constexpr (WK == 1) {
 #pragma unroll
@@ -294,18 +328,19 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
 // column tiles; rows of 256 bytes have their 16-byte chunks XOR-swizzled by
 // the row, which spreads the 16 rows of a fragment over the banks. Row blocks
 // are dealt to the workgroups of grid dimension y. 512 tokens, top-4 of 8
-// experts of 2048 x 1024: 54 us for both products and the sum, 480 TFLOP/s,
-// bound by the length of a step: without three quarters of the products it
-// takes 46 us, without the loads 47, without the decoding 54, and two steps a
-// barrier, or loads two steps ahead, are slower (69, 56).
+// experts of 2048 x 1024: 71 us for both products and the sum, 360 TFLOP/s (480
+// with H's second term counted), bound by the length of a step: with one term,
+// 54 us in all, it takes 46 without three quarters of the products, 47 without
+// the loads, 54 without the decoding, and two steps a barrier, or loads two
+// steps ahead, are slower (69, 56).
 constexpr int kManyRows = 64;
 template <bool GATE_UP> constexpr int kManyTiles = GATE_UP ? 1 : 2;   // tiles a wave
 template <bool GATE_UP>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
-  constexpr int NM = GATE_UP ? 2 : 1, NT = kManyTiles<GATE_UP>, RB = kManyRows / 16;   // matrices, tiles, row blocks
+  constexpr int NM = GATE_UP ? 2 : 1, NT = kManyTiles<GATE_UP>, RB = kManyRows / 16, NX = kTerms<GATE_UP>;   // matrices, tiles, row blocks
   __shared__ uint16_t list[MOE_W4_MAX_SLOTS];
   __shared__ int count[4];
-  __shared__ w4u32x4_t xs[2][kManyRows * 16];
+  __shared__ w4u32x4_t xs[2][NX][kManyRows * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int K = GATE_UP ? a.d : a.F, N = GATE_UP ? a.F : a.d;
   const int tiles = N / kTileN, groups = (tiles + 4 * NT - 1) / (4 * NT);
@@ -321,14 +356,16 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
 #pragma unroll
     for (int i = 0; i < RB; ++i) {   // a row past the last reads the last one
       const int s = list[min(r0 + sr + 16 * i, rows.n - 1)];
-      src[i] = reinterpret_cast<const w4u32x4_t*>(GATE_UP ? a.x + (size_t)(s / a.k) * K : a.h + (size_t)s * K) + sc;
+      src[i] = w4_row<GATE_UP, w4u32x4_t>(a, s) + sc;
     }
-    w4u32x4_t xv[RB];
+    w4u32x4_t xv[NX][RB];
     V16 qv[NM][NT];
     uint32_t sv[NM][NT];
     auto fetch = [&](int st) {
 #pragma unroll
-      for (int i = 0; i < RB; ++i) xv[i] = src[i][st * 16];
+      for (int x = 0; x < NX; ++x)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) xv[x][i] = src[i][x * (K / 8) + st * 16];
 #pragma unroll
       for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -348,9 +385,11 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
     __syncthreads();   // the block before is read
     fetch(0);
     for (int st = 0; st < steps; ++st) {
-      w4u32x4_t* buf = xs[st & 1];
+      w4u32x4_t(&buf)[NX][kManyRows * 16] = xs[st & 1];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) buf[(sr + 16 * i) * 16 + (sc ^ sr)] = xv[i];
+      for (int x = 0; x < NX; ++x)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) buf[x][(sr + 16 * i) * 16 + (sc ^ sr)] = xv[x][i];
       V16 qc[NM][NT];
       float scale[NM][NT];
 #pragma unroll
@@ -364,18 +403,22 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
       if (st + 1 < steps) fetch(st + 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        w4bf16x8_t xf[RB];
+        w4bf16x8_t xf[NX][RB];
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-          xf[r] = __builtin_bit_cast(w4bf16x8_t, buf[(16 * r + (lane & 15)) * 16 + (((lane >> 4) * 4 + j) ^ (lane & 15))]);
+        for (int x = 0; x < NX; ++x)
+#pragma unroll
+          for (int r = 0; r < RB; ++r)
+            xf[x][r] = __builtin_bit_cast(w4bf16x8_t, buf[x][(16 * r + (lane & 15)) * 16 + (((lane >> 4) * 4 + j) ^ (lane & 15))]);
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             const w4bf16x8_t w = decode_w4(qc[m][i].w[j], scale[m][i]);
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
-              acc[m][i][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf[r], acc[m][i][r], 0, 0, 0);
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+              for (int r = 0; r < RB; ++r)
+                acc[m][i][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf[x][r], acc[m][i][r], 0, 0, 0);
           }
       }
     }
@@ -396,10 +439,10 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
 }
 
 // The down product and the weighted sum at once, for a handful of slots. One
-// token: 4.6 us, of which 2.7 are a launch's own and the weights' bytes 0.9. A
+// token: 4.7 us, of which 2.7 are a launch's own and the weights' bytes 0.9. A
 // workgroup takes 16 output columns, its waves the (slot, chunk of K) pairs in
-// turn, every row of the product the same slot's H. A slot's sums over K are
-// added in order, then the token's slots.
+// turn, the places of the product's rows all the same slot's H, first or second
+// term. A slot's sums over K are added in order, then the token's slots.
 constexpr int kOneWaves = 8;
 __global__ void __launch_bounds__(64 * kOneWaves) w4_down_sum_kernel(W4Args a) {
   __shared__ float red[MOE_MAX_TOPK * kW4SumParts][kTileN];
@@ -412,7 +455,7 @@ __global__ void __launch_bounds__(64 * kOneWaves) w4_down_sum_kernel(W4Args a) {
     const int e = a.idx[s];
     if (e < 0 || e >= a.E) continue;
     const size_t t = (size_t)e * tiles + blockIdx.x;
-    const V16* src = reinterpret_cast<const V16*>(a.h + (size_t)s * a.F) + (lane >> 4) * 4;
+    const V16* src = w4_row<false, V16>(a, s) + (lane >> 4) * 4 + (lane & 15) / 8 * (a.F / 8);
     w4f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     for (int c = part; c < chunks; c += parts) {
       const uint32_t sw = reinterpret_cast<const uint32_t*>(a.wd.s)[(t * chunks + c) * 64 + lane];
@@ -434,6 +477,7 @@ __global__ void __launch_bounds__(64 * kOneWaves) w4_down_sum_kernel(W4Args a) {
                                                         acc, 0, 0, 0);
       }
     }
+    acc = add_terms(acc);
     if ((lane & 15) == 0)
 #pragma unroll
       for (int r = 0; r < 4; ++r) red[it][4 * (lane >> 4) + r] = acc[r];
@@ -514,7 +558,7 @@ template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
   MOE_CHECK_SUPPORTED(units * tiles < (1L << 31));
   constexpr int kCols = 4 * kManyTiles<GATE_UP>;
   const int groups = (tiles + kCols - 1) / kCols;
-  if (R <= (units * groups >= 512 ? kFewRows : kFewRowsSmall) * a.E) {
+  if (R <= (units * groups >= 512 ? kFewRows : kFewRowsSmall) / kTerms<GATE_UP> * a.E) {
     const long bytes = units * 3 * a.d * (long)a.F * 17 / 32;
     // codes past the caches: 167 MB 47 us against 43, 372 MB 78 against 72, but
     // 53 MB, which three weight sets in turn leave in them, 19 against 21
@@ -528,8 +572,8 @@ template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
   return launch_status();
 }
 
-// Workspace: H rows, then from a 16-byte boundary the slots' output rows.
-size_t w4_part_offset(int T, int k, int F) { return ((size_t)T * k * F * 2 + 15) & ~static_cast<size_t>(15); }
+// Workspace: H rows (two bf16 terms), then from a 16-byte boundary the slots' output rows.
+size_t w4_part_offset(int T, int k, int F) { return ((size_t)T * k * F * 4 + 15) & ~static_cast<size_t>(15); }
 
 }  // namespace
 }  // namespace moe

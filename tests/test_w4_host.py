@@ -28,7 +28,7 @@ def test_sizes():
     assert lib.moe_w4_scale_bytes(512, 16) == 256 and lib.moe_w4_scale_bytes(640, 32) == 1024
     assert lib.moe_w4_code_bytes(0, 16) == 0 and lib.moe_w4_scale_bytes(128, -1) == 0
     assert lib.moe_experts_w4_workspace_bytes(0, 2, 128, 128) == 0
-    assert lib.moe_experts_w4_workspace_bytes(3, 2, 256, 128) == 6 * 128 * 2 + 6 * 256 * 4
+    assert lib.moe_experts_w4_workspace_bytes(3, 2, 256, 128) == 6 * 128 * 4 + 6 * 256 * 4
 
 
 def test_quantize_argument_errors():
