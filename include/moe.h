@@ -93,7 +93,8 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float
 /* ----------------------------------------------------------------- norm
  * moe_add_rmsnorm: what a block runs on its token rows before the layer.
  *   h[t] = x[t] + res[t], rounded to `dtype`     (res given)
- *   rs   = 1 / sqrt(mean_i(h[t,i]^2) + eps)      (of h as it is stored; the sum in binary64)
+ *   rs   = 1 / sqrt(mean_i(h[t,i]^2) + eps)      (of h as it is stored: binary32 squares,
+ *                                                 summed in binary64)
  *   y[t,i] = h[t,i] * rs * w[i], rounded once to `dtype`
  * With res NULL, h is x itself and must be NULL here. The MXFP8 copy (q, s),
  * bf16 with d % 128 == 0 only, holds the rows of y exactly as moe_mx_quantize

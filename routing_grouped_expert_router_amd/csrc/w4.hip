@@ -17,6 +17,8 @@
 // holds its scales for four such steps.
 #include "mx_common.h"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -29,15 +31,16 @@ constexpr int kTileN = 16;      // columns of a tile
 constexpr int kStepK = 128;     // K values of a step
 constexpr int kChunk = 4;       // steps that share a scale word
 constexpr int kW4Threads = 256;
-// Slots an expert, on average, up to which rows go 16 at a time: the 64-row
-// kernel takes over where its workgroups fill the chip, later where they do
-// not, and for the down product, whose two terms make it 8 rows at a time, at
-// half as many. Measured (d 2048, F 1024, the call's time with 16 or 8 at a time
-// against 64): gate/up, 32 experts, 10 slots each, 42 us against 47, 16 slots 52
-// against 49; 8 experts, 16 slots, 27 against 31, 32 slots 31.3 against 30.9.
-// Down, 32 experts, 6 slots, 35 against 39, 8 slots 41 against 39; 8 experts,
-// 10 slots, 20 against 22, 16 slots 26.8 against 26.2, 20 slots 30 against 27.
-constexpr int kFewRows = 12, kFewRowsSmall = 30;
+// Slots an expert, on average, up to which a product goes 16 rows (8 of H's two
+// terms) at a time: beyond, the kernel that shares decoded weights among more
+// rows takes over, for gate/up later where its workgroups do not fill the chip.
+// Measured (d 2048, F 1024, the call's time with few rows at a time against
+// many): gate/up, 32 experts, 12 slots each, 38.0 us against 38.7, 16 slots 45
+// against 41; 8 experts, 24 slots, 24.6 against 26.1, 32 slots 28.1 against
+// 26.5. Down, 128 experts, 6 slots, 99 against 106, 8 slots 111 against 104; 32
+// experts, 4 slots, 31.6 against 31.1, 6 slots 34.6 against 31.6; 8 experts, 8
+// slots, 18.6 against 18.7, 12 slots 21.5 against 19.7.
+constexpr int kFewRows = 12, kFewRowsSmall = 30, kFewRowsDown = 6;
 // The down product and the weighted sum are one launch while few slots share
 // an expert's weights, which that launch reads once a slot: up to half the
 // experts, or up to two slots an expert where the caches keep the pool's down
@@ -322,25 +325,25 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_few_kernel(W4Args a) {
   }
 }
 
-// Many rows an expert (short prompts, small pools). 64 rows at a time, so that
-// a decoded weight serves four products. The rows' 128-value steps go through
-// two LDS buffers that the four waves share, each wave runs down its own
-// column tiles; rows of 256 bytes have their 16-byte chunks XOR-swizzled by
-// the row, which spreads the 16 rows of a fragment over the banks. Row blocks
-// are dealt to the workgroups of grid dimension y. 512 tokens, top-4 of 8
-// experts of 2048 x 1024: 71 us for both products and the sum, 360 TFLOP/s (480
-// with H's second term counted), bound by the length of a step: with one term,
-// 54 us in all, it takes 46 without three quarters of the products, 47 without
-// the loads, 54 without the decoding, and two steps a barrier, or loads two
-// steps ahead, are slower (69, 56).
-constexpr int kManyRows = 64;
-template <bool GATE_UP> constexpr int kManyTiles = GATE_UP ? 1 : 2;   // tiles a wave
-template <bool GATE_UP>
+// Many rows an expert (short prompts, small pools). ROWS at a time, so that a
+// decoded weight serves three or four products (48 rows of x, 32 of H in two
+// terms; 64 of either are 3 to 30 % slower, fewer waves being at work). The rows'
+// 128-value steps go through two LDS buffers that the four waves share, each
+// wave runs down its own NT column tiles; rows of 256 bytes have their 16-byte
+// chunks XOR-swizzled by the row, which spreads the 16 rows of a fragment over
+// the banks. Row blocks are dealt to the workgroups of grid dimension y. 512
+// tokens, top-4 of 8 experts of 2048 x 1024: 62 us for both products and the
+// sum, 410 TFLOP/s (550 with H's second term counted), bound by the length of a
+// step: with 64 rows and one term, 54 us, it took 46 without three quarters of
+// the products, 47 without the loads, 54 without the decoding, and two steps a
+// barrier, or loads two steps ahead, were slower (69, 56).
+template <bool GATE_UP> constexpr int kManyRows = GATE_UP ? 48 : 32;
+template <bool GATE_UP, int NT>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
-  constexpr int NM = GATE_UP ? 2 : 1, NT = kManyTiles<GATE_UP>, RB = kManyRows / 16, NX = kTerms<GATE_UP>;   // matrices, tiles, row blocks
+  constexpr int NM = GATE_UP ? 2 : 1, ROWS = kManyRows<GATE_UP>, RB = ROWS / 16, NX = kTerms<GATE_UP>;
   __shared__ uint16_t list[MOE_W4_MAX_SLOTS];
   __shared__ int count[4];
-  __shared__ w4u32x4_t xs[2][NX][kManyRows * 16];
+  __shared__ w4u32x4_t xs[2][NX][ROWS * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int K = GATE_UP ? a.d : a.F, N = GATE_UP ? a.F : a.d;
   const int tiles = N / kTileN, groups = (tiles + 4 * NT - 1) / (4 * NT);
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
   const size_t t0 = (size_t)rows.e * tiles;
   const W4Mat mat[2] = {GATE_UP ? a.wg : a.wd, a.wu};
   const int sr = tid >> 4, sc = tid & 15;   // staging: rows sr + 16 i, chunk sc
-  for (int r0 = blockIdx.y * kManyRows; r0 < rows.n; r0 += gridDim.y * kManyRows) {
+  for (int r0 = blockIdx.y * ROWS; r0 < rows.n; r0 += gridDim.y * ROWS) {
     const w4u32x4_t* src[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {   // a row past the last reads the last one
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_many_kernel(W4Args a) {
     __syncthreads();   // the block before is read
     fetch(0);
     for (int st = 0; st < steps; ++st) {
-      w4u32x4_t(&buf)[NX][kManyRows * 16] = xs[st & 1];
+      w4u32x4_t(&buf)[NX][ROWS * 16] = xs[st & 1];
 #pragma unroll
       for (int x = 0; x < NX; ++x)
 #pragma unroll
@@ -556,18 +559,30 @@ template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
   const int wk = chunks >= 3 ? 4 : chunks;   // waves that share a tile's K: as many as it has chunks, up to 4
   const long units = min(R, a.E);
   MOE_CHECK_SUPPORTED(units * tiles < (1L << 31));
-  constexpr int kCols = 4 * kManyTiles<GATE_UP>;
-  const int groups = (tiles + kCols - 1) / kCols;
-  if (R <= (units * groups >= 512 ? kFewRows : kFewRowsSmall) / kTerms<GATE_UP> * a.E) {
+  auto groups_of = [&](int nt) { return (tiles + 4 * nt - 1) / (4 * nt); };
+  const int few = !GATE_UP ? kFewRowsDown : units * groups_of(1) >= 512 ? kFewRows : kFewRowsSmall;
+  if (R <= few * a.E) {
     const long bytes = units * 3 * a.d * (long)a.F * 17 / 32;
     // codes past the caches: 167 MB 47 us against 43, 372 MB 78 against 72, but
     // 53 MB, which three weight sets in turn leave in them, 19 against 21
     if (bytes >= kStreamBytes) launch_few<GATE_UP, true>(a, wk, units, tiles, s);
     else launch_few<GATE_UP, false>(a, wk, units, tiles, s);
   } else {
-    const int blocks = (R + kManyRows - 1) / kManyRows;
-    const long want = (1024 + units * groups - 1) / (units * groups);   // four workgroups a CU
-    w4_many_kernel<GATE_UP><<<dim3((unsigned)(units * groups), (unsigned)min((long)blocks, want)), kW4Threads, 0, s>>>(a);
+    auto many = [&](auto nt) {
+      const long wg = units * groups_of(nt);
+      const long blocks = (R + kManyRows<GATE_UP> - 1) / kManyRows<GATE_UP>, want = (1024 + wg - 1) / wg;   // four workgroups a CU
+      w4_many_kernel<GATE_UP, nt><<<dim3((unsigned)wg, (unsigned)min(blocks, want)), kW4Threads, 0, s>>>(a);
+    };
+    using std::integral_constant;
+    if constexpr (GATE_UP) {
+      many(integral_constant<int, 1>());
+    } else {
+      // four tiles where their workgroups, over the rows there are, still cover
+      // the CUs (512 tokens of 8 experts 61.6 us against 65.5 with two, 512 of
+      // 32 74 against 80; 128 of 8 31.4 against 30.0, 128 of 32 40.0 against 38.9)
+      if ((long)R * groups_of(4) >= 256L * kManyRows<GATE_UP>) many(integral_constant<int, 4>());
+      else many(integral_constant<int, 2>());
+    }
   }
   return launch_status();
 }

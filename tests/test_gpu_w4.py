@@ -82,10 +82,12 @@ def check(y, ref, mag, hmag, K_d, K_F):
     assert np.all(np.abs(y - ref) <= 2.0 ** -8 * (np.abs(ref) + tol) + tol)
 
 
-CASES = [  # T, d, E, k, F: one token; slots up to the experts; more; rows past 16 and 64; K of 1 to 9 steps; one expert
+CASES = [  # T, d, E, k, F: one token; slots up to the experts; more; rows past 16 and 64; K of 1 to 9 steps; one
+    # expert; a thousand tokens
     (1, 256, 8, 2, 128), (1, 2048, 4, 4, 1024), (1, 128, 1, 1, 128), (3, 1152, 12, 4, 640), (2, 128, 4, 4, 512),
     (16, 256, 4, 1, 256), (17, 256, 1, 1, 384), (70, 640, 3, 2, 128), (150, 128, 2, 2, 256), (9, 1024, 64, 8, 128),
     (64, 256, 128, 4, 128), (40, 384, 8, 8, 1152), (1, 4096, 2, 2, 128), (130, 1152, 3, 2, 384), (200, 256, 2, 2, 640),
+    (1000, 640, 8, 4, 128), (900, 1152, 3, 2, 256),
 ]
 
 
