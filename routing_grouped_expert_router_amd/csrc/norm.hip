@@ -8,9 +8,9 @@
 // Memory-bound in both directions: every element is read and written once, and
 // a whole row stays in the registers of the 1 to 12 waves that share it, so
 // the norm and the quantisation cost no second pass. 16384 x 2048 bf16 with a
-// residual: forward 42.9 us (6.3 TB/s; a plain copy reaches 5.1), 51 to 54
-// with the MXFP8 copy, backward 48.3 us with dw; one token 2.7 us, a launch's own
-// time. See include/moe.h for the contract of each entry point.
+// residual: forward 42.9 us (6.3 TB/s; a plain copy reaches 5.1), 51 to 56
+// with the MXFP8 copy, backward 48.3 us with dw; one token 3.0 us, 2.7 of them a
+// launch's own. See include/moe.h for the contract of each entry point.
 #include "mx_common.h"
 
 #include <type_traits>
