@@ -242,13 +242,28 @@ int launch_dma(const moe_gg_desc* g, const GGArgs& a, bool kvar, bool dual, int 
 }
 
 // The two ops that keep G and U in 8 bits (N / bno column tiles).
-int launch_ckpt(const moe_gg_desc* g, const GGArgs& a, int tiles_n, hipStream_t stream) {
-  using C = WithCkpt<CfgDma>;
-  const long grid = ((g->n_rows + C::BM - 1) / C::BM + g->E) * (long)tiles_n;
+template <class C> long ckpt_grid(const moe_gg_desc* g, int tiles_n) {
+  return ((g->n_rows + C::BM - 1L) / C::BM + g->E) * tiles_n;
+}
+template <class C> int launch_ckpt_tiles(const moe_gg_desc* g, const GGArgs& a, int tiles_n, hipStream_t stream) {
+  const long grid = ckpt_grid<C>(g, tiles_n);
   MOE_CHECK_SUPPORTED(grid < (1L << 31));
   if (g->op == MOE_GG_FWD_GATE_UP) gg_dma_kernel<MOE_GG_FWD_GATE_UP, C><<<(int)grid, C::NT, 0, stream>>>(a);
   else gg_dma_kernel<MOE_GG_DGRAD_DOWN, C><<<(int)grid, C::NT, 0, stream>>>(a);
   return launch_status();
+}
+
+// Half the rows and twice the depth of a K step where that gives at most one
+// workgroup to each of the 256 CUs: nothing then hides a workgroup's own
+// latency, and its barriers and its epilogue are halved. Both GEMMs, 1021 rows,
+// d 256, F 256, 16 experts: 29.9 us with 128-row tiles, 20.9 so; gate/up, 2048
+// rows, d 512, F 512, 16 experts (192 workgroups): 3.7 us less, 4096 rows, d 1024
+// (320): 8.6 more; data gradient, 4096 rows, d 1024, F 512, 16 experts (160): 11
+// less, 8192 rows (288): 2.0 more.
+using CfgDmaSmall = DmaCfg<64, 256, 2, 4, 64, 3, 1>;
+int launch_ckpt(const moe_gg_desc* g, const GGArgs& a, int tiles_n, hipStream_t stream) {
+  if (ckpt_grid<CfgDmaSmall>(g, tiles_n) <= 256) return launch_ckpt_tiles<WithCkpt<CfgDmaSmall>>(g, a, tiles_n, stream);
+  return launch_ckpt_tiles<WithCkpt<CfgDma>>(g, a, tiles_n, stream);
 }
 
 template <int OP> struct LaunchSimpleBf16 {

@@ -55,8 +55,9 @@ template <int BM_, int BN_, int WM_, int WN_, int BK_, int ST_, int OCC_ = 1> st
   static_assert(WMR % 32 == 0 && WNR % 64 == 0, "wave tile");
   static_assert((BK * BN / 16) % 64 == 0, "dual sub-tiles hold whole wave-loads");
   // the MN-contiguous swizzle XORs chunk indices with up to 12: rows of an
-  // MN-contiguous tile (A: BM, B: BN or BN/2 for the dual ops) need >= 16 chunks
-  static_assert(BM >= 128 && BN / 2 >= 128, "MN-contiguous rows of >= 16 chunks");
+  // MN-contiguous tile (A: BM, asserted where A is one, B: BN or BN/2 for the
+  // dual ops) need >= 16 chunks
+  static_assert(BN / 2 >= 128, "MN-contiguous rows of >= 16 chunks");
   static_assert(OCC * (LDS_ELEMS * 2 + 4 * (MOE_MAX_EXPERTS + 1)) <= 160 * 1024, "LDS");
   static_assert(WNR <= CW && (BN <= CW || BN % CW == 0), "wave columns within one staging chunk");
 };
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(C::NT, C::WAVES_PER_SIMD) gg_dma_kernel(GGArgs
   constexpr int MI = C::MI, NI = C::NI, CPR = C::CPR;
   constexpr int BNO = DUAL ? BN / 2 : BN;          // output columns per matrix per tile
   constexpr int A_ELEMS = BM * BK;
+  static_assert(AK || BM >= 128, "MN-contiguous rows of >= 16 chunks");
   __shared__ int tile_start[MOE_MAX_EXPERTS + 1];
   __shared__ __attribute__((aligned(1024))) uint16_t lds[C::LDS_ELEMS];
 

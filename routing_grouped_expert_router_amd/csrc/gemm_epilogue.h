@@ -260,17 +260,17 @@ MOE_DEV void gg_store_tile(const GGArgs& a, const df32x16_t (&acc)[C::MI][C::NI]
     }
   } else if constexpr (OP == MOE_GG_DGRAD_DOWN && C::kCkpt && !C::kMxCopies) {
     // G and U from their 8-bit rows, and H from them again for the weight
-    // gradient. A pass takes the rows of one 32-row block of every wave (64
-    // rows of all BN columns), so that each wave works in both passes: with
-    // the passes over columns half of them idle, 2.4 us more where a tile or
-    // two is all a CU has.
-    static_assert(MI == 2 && C::WM == 2 && BM == 128 && 2 * (BM / 2) * (BN + 8) <= 2 * BM * LDW, "two planes of 64 rows");
-    constexpr int PR = BM / 2, LDP = BN + 8, CPRW = BN / 8;
+    // gradient. A pass takes the rows of one 32-row block of every wave (of
+    // all BN columns), so that each wave works in every pass: with passes over
+    // columns half of them idle, 2.4 us more where a tile or two is all a CU
+    // has.
+    constexpr int PR = BM / MI, LDP = BN + 8, CPRW = BN / 8;
+    static_assert(2 * PR * LDP <= C::LDS_ELEMS, "the planes of a pass");
     uint16_t* pg = lds;
     uint16_t* pu = lds + PR * LDP;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      auto tile_row = [&](int pr) { return (pr >> 5) * 64 + p * 32 + (pr & 31); };
+    for (int p = 0; p < MI; ++p) {
+      auto tile_row = [&](int pr) { return (pr >> 5) * C::WMR + p * 32 + (pr & 31); };
       for (int q = tid; q < PR * CPRW; q += NT) {
         const int r = q / CPRW, c = q % CPRW, tr = tile_row(r);
         if (tr >= rows_valid) continue;
@@ -309,7 +309,7 @@ MOE_DEV void gg_store_tile(const GGArgs& a, const df32x16_t (&acc)[C::MI][C::NI]
         *reinterpret_cast<V16*>((uint16_t*)a.dg + o) = *reinterpret_cast<const V16*>(pg + r * LDP + c * 8);
         *reinterpret_cast<V16*>((uint16_t*)a.du + o) = *reinterpret_cast<const V16*>(pu + r * LDP + c * 8);
       }
-      if (p == 0) __syncthreads();
+      if (p + 1 < MI) __syncthreads();
     }
   } else if (OP == MOE_GG_DGRAD_DOWN) {
     // per column chunk: stage G and U, turn them into dG and dU in place

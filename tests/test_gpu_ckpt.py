@@ -49,7 +49,8 @@ def problem(counts, d, F, seed, spare=0):
     return E, n, dev(off, "i32"), x, dy, wg, wu, wd
 
 
-COUNTS = [[1], [0, 3, 0], [129, 0, 127, 1, 256], [5, 300, 0, 64], [700]]
+# the last for tiles of 64 rows (F 256), of 128 (F 1024), and of both (F 768)
+COUNTS = [[1], [0, 3, 0], [129, 0, 127, 1, 256], [5, 300, 0, 64], [700], [2100, 0, 1999]]
 
 
 @pytest.mark.parametrize("counts", COUNTS, ids=str)
