@@ -248,9 +248,9 @@ def _same_device(*tensors):
 def _fill(desc, fields):
     """Set descriptor pointer fields once every tensor has passed its layout
     check; raise if any of them is in host memory."""
-    if any(v is _HOST for _, v in fields):
-        raise MoEError("libmoe needs device tensors")
-    for obj, name, v in ((o, n, v) for (o, n), v in fields):
+    for (obj, name), v in fields:
+        if v is _HOST:
+            raise MoEError("libmoe needs device tensors")
         setattr(obj, name, v)
 
 
@@ -419,9 +419,7 @@ _GG_NUMEL = {
 
 def make_gg_desc(op, dtype, E, d, F, n_rows, capacity=0, group_offsets=None, ws=None,
                  **tensors) -> moe_gg_desc:
-    desc = moe_gg_desc()
-    desc.op, desc.dtype, desc.E, desc.d, desc.F = op, dtype, E, d, F
-    desc.n_rows, desc.capacity = n_rows, capacity
+    desc = moe_gg_desc(op, dtype, E, d, F, n_rows, capacity)
     fields = [((desc, "group_offsets"), _req(group_offsets, "group_offsets", torch.int32, E + 1, optional=True))]
     tdt = torch.bfloat16 if dtype == MOE_BF16 else torch.float32
     for name, t in tensors.items():
@@ -448,10 +446,11 @@ def _ckpt(desc, g: MxTensor, u: MxTensor):
     """The 8-bit rows of G and U as descriptors, checked against desc's sizes."""
     n, u8 = desc.n_rows * desc.F, torch.uint8
     _same_device(g.q, g.s, u.q, u.s)
-    mg, mu = moe_mx_tensor(), moe_mx_tensor()
-    _fill(None, [((m, f), _req(getattr(t, f), f"{name}.{f}", u8, min_numel=size))
-                 for m, t, name in ((mg, g, "g"), (mu, u, "u")) for f, size in (("q", n), ("s", n // 32))])
-    return C.byref(mg), C.byref(mu)
+    at = (_req(g.q, "g.q", u8, min_numel=n), _req(g.s, "g.s", u8, min_numel=n // 32),
+          _req(u.q, "u.q", u8, min_numel=n), _req(u.s, "u.s", u8, min_numel=n // 32))
+    if _HOST in at:
+        raise MoEError("libmoe needs device tensors")
+    return C.byref(moe_mx_tensor(at[0], at[1])), C.byref(moe_mx_tensor(at[2], at[3]))
 
 
 def moe_grouped_gemm_ckpt(desc: moe_gg_desc, g: MxTensor, u: MxTensor, stream=None):
