@@ -403,11 +403,16 @@ class MoELayer:
 
     def release_intermediates(self):
         """Drop the step's activations and the backward's scratch (x_perm,
-        G, U, H, y_perm, y, dY_perm, dG, dU, dX_perm); the next step
-        allocates them again from torch's caching allocator."""
+        G, U, H, y_perm, y, the 8-bit copies of act8, dY_perm, dG, dU,
+        dX_perm); the next step allocates them again from torch's caching
+        allocator."""
         self.x_perm = self.g = self.u = self.h = self.y_perm = self.y = None
         self.dy_perm = self.dg = self.du = self.dx_perm = None
         self.x8 = self._x8 = self.g8 = self.u8 = self.g8_s = self.u8_s = None
+        if self.mxfp8:   # the experts' names for the same tensors
+            mx = self.mx
+            mx.g = mx.u = mx.h = mx.y_perm = mx.g8 = mx.u8 = None
+            mx.dg = mx.du = mx.dx_perm = None
 
     def experts_backward(self):
         self.experts_backward_data()

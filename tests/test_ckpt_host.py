@@ -1,5 +1,7 @@
 """Refusals of the 8-bit activation checkpoint, on the host."""
 import ctypes as C
+import gc
+import weakref
 
 import pytest
 import torch
@@ -103,3 +105,27 @@ def test_layer_takes_rows_only_with_act8():
     lay = MoELayer(8, 256, 4, 2, 256, device="cpu", routing="given")
     with pytest.raises(ValueError, match="act8"):
         lay.forward(None, None, None, None, x8=object())
+
+
+@pytest.mark.parametrize("opts", [dict(), dict(act8=True), dict(mx_bf16_intermediates=False),
+                                  dict(act8=True, mx_bf16_intermediates=False)], ids=str)
+def test_release_lets_go_of_the_mxfp8_experts_tensors_too(opts):
+    """What the layer releases is held by nothing else: the MXFP8 experts
+    write into the same tensors under names of their own."""
+    lay = MoELayer(8, 256, 4, 2, 256, device="cpu", routing="given", mxfp8=True, **opts)
+    lay.forward_buffers()
+    lay.backward_buffers()
+    held = {}
+    for name in ("g", "u", "h", "y_perm", "y", "dy_perm", "dg", "du", "dx_perm"):
+        if getattr(lay, name) is not None:
+            held[name] = weakref.ref(getattr(lay, name))
+    for name in ("g8", "u8") if lay.act8 else ():
+        held[name] = weakref.ref(getattr(lay, name).q)
+    assert len(held) >= 6
+    lay.release_intermediates()
+    gc.collect()
+    assert [n for n, r in held.items() if r() is not None] == []
+    lay.forward_buffers()                                       # and the next step has them again
+    lay.backward_buffers()
+    assert lay.mx.y_perm is lay.y_perm and lay.mx.dx_perm is lay.dx_perm and lay.mx.dg is lay.dg
+    assert (lay.mx.g8 is lay.g8 and lay.g8 is not None) if lay.act8 else lay.mx.g is lay.g

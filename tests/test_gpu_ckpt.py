@@ -359,3 +359,27 @@ def test_block_captured_and_replayed():
         got = list(out) + list(held.layer.grads().values())
         for a, b in zip(got, want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("act8", [False, True])
+def test_mxfp8_layer_releases_its_step(act8):
+    """With keep_intermediates=False nothing but the gradients is left of a
+    step, and a second step peaks where the first did."""
+    T, d, E, k, F = 2048, 1024, 8, 4, 1024
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF) * 0.05
+    x, dy, ws = rand(T, d), rand(T, d), (rand(E, d, F), rand(E, d, F), rand(E, F, d))
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    p = torch.full((T, k), 1 / k, device="cuda")
+    lay = MoELayer(T, d, E, k, F, routing="given", mxfp8=True, act8=act8, keep_intermediates=False)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    peaks = []
+    for _ in range(3):
+        torch.cuda.reset_peak_memory_stats()
+        lay.forward(x, *ws, topk_idx=idx, topk_w=p)
+        lay.backward(dy)
+        peaks.append(torch.cuda.max_memory_allocated())
+        left = torch.cuda.memory_allocated() - before
+        assert left <= sum(v.numel() * v.element_size() for v in lay.grads().values()) + (1 << 20)
+    assert peaks[1] <= peaks[0] and peaks[2] <= peaks[0]
