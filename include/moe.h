@@ -93,17 +93,17 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float
 /* ----------------------------------------------------------------- norm
  * moe_add_rmsnorm: what a block runs on its token rows before the layer.
  *   h[t] = x[t] + res[t], rounded to `dtype`     (res given)
- *   rs   = 1 / sqrt(mean_i(h[t,i]^2) + eps)      (of h as it is stored: binary32 squares,
- *                                                 summed in binary64)
+ *   rs   = 1 / sqrt(mean_i(h[t,i]^2) + eps)      (of h as it is stored: squares, sums and
+ *                                                 root in binary64)
  *   y[t,i] = h[t,i] * rs * w[i], rounded once to `dtype`
  * With res NULL, h is x itself and must be NULL here. The MXFP8 copy (q, s),
  * bf16 with d % 128 == 0 only, holds the rows of y exactly as moe_mx_quantize
  * axis 0 writes them from the rounded y: codes q [T,d], scales s of T*d/32
  * bytes; both or neither NULL. y may be NULL when the copy is given. rstd [T]
- * binary32 (may be NULL) receives rs for the backward pass.
+ * binary32 (may be NULL) receives rs, rounded, for the backward pass.
  *   x, res, h, y [T,d] and w [d] of `dtype`; d <= MOE_MAX_NORM_D; eps > 0.
  * h and y may each be x or res itself (not both the same one); other overlaps
- * are not allowed. Values whose squares overflow binary32 give rs = 0.
+ * are not allowed.
  *
  * moe_add_rmsnorm_bwd: derived, its adjoint, with n = h * rs and g = dy * w:
  *   dx[t] = dh[t] + rs * (g - n * mean_i(g * n)), rounded once to `dtype`:

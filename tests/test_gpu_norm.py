@@ -267,3 +267,52 @@ def test_permute_from_mx(T, d, k, E, cap):
         L.moe_permute_from_mx(q, k, bad, None, again)
         want[r] = 5.0
         assert torch.equal(again, want)
+
+
+# ----------------------------------------------------------------------------- accuracy and range
+def run_forward(x, w, kind, eps):
+    """(y, rstd) of the kernel and of the definition in 64 bits, at the eps it is given in binary32."""
+    T, d = x.shape
+    y, rstd = torch.empty(T, d, dtype=TDT[kind], device="cuda"), torch.empty(T, device="cuda")
+    L.moe_add_rmsnorm(put(x, kind), put(w, kind), eps, y=y, rstd=rstd)
+    rs = 1 / np.sqrt(np.mean(x * x, axis=1) + float(np.float32(eps)))
+    return host(y), host(rstd), x * rs[:, None] * w, rs
+
+
+def check_root(rstd, rs_ref):
+    """rstd is the 64-bit root rounded to binary32: half a step, 2^-10 of that
+    for what the 64-bit operations leave, and half the smallest value."""
+    assert np.all(np.abs(rstd - rs_ref) <= U * (1 + 2.0 ** -10) * rs_ref + 2.0 ** -150)
+
+
+def check_rows(y, rstd, y_ref, rs_ref, kind):
+    """y takes half a step, the root's rounding (2 U where it is subnormal) and
+    two products' roundings."""
+    check_root(rstd, rs_ref)
+    assert np.all(np.abs(y - y_ref) <= (STEP[kind] + 5 * U) * np.abs(y_ref) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 1000, 2056, 8200])
+def test_squares_past_binary32(d, kind):
+    """Rows whose squares, or whose sums of a few squares, leave binary32 at
+    either end."""
+    g = np.random.default_rng([14, d])
+    r = ROUND[kind]
+    w = r(1 + 0.2 * g.standard_normal(d))
+    unit = r(np.clip(g.standard_normal((6, d)), -3, 3))
+    check_rows(*run_forward(r(unit * np.array([[1e18], [1e19], [3e19], [1e25], [1e37], [1e38]])), w, kind, EPS), kind)
+    same = np.broadcast_to(r(np.full((1, 1), 1e19)), (1, d))       # each square is finite, eight of them are not
+    check_rows(*run_forward(same, w, kind, EPS), kind)
+    check_rows(*run_forward(r(unit * np.array([[1e-19], [1e-20], [1e-21], [1e-22], [1e-25], [1.0]])), w, kind, 1e-40),
+               kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(2048, 2048), (300, 2056), (64, 8200)])
+def test_root_is_the_definitions_rounded(T, d, kind):
+    """A sum that passes through binary32 leaves some rows' roots past the bound."""
+    g = np.random.default_rng([13, T, d])
+    x = ROUND[kind](g.standard_normal((T, d)) * np.where(g.random(d) < 0.02, 30.0, 1.0))
+    _, rstd, _, rs_ref = run_forward(x, np.ones(d), kind, EPS)
+    check_root(rstd, rs_ref)
