@@ -92,10 +92,11 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float
 
 /* ----------------------------------------------------------------- norm
  * moe_add_rmsnorm: what a block runs on its token rows before the layer.
- *   h[t] = x[t] + res[t], rounded to `dtype`     (res given)
+ *   h[t] = x[t] + res[t], a binary32 sum rounded to `dtype` (res given)
  *   rs   = 1 / sqrt(mean_i(h[t,i]^2) + eps)      (of h as it is stored: squares, sums and
  *                                                 root in binary64)
- *   y[t,i] = h[t,i] * rs * w[i], rounded once to `dtype`
+ *   y[t,i] = h[t,i] * rs * w[i], a binary64 product rounded to binary32 and, for bf16,
+ *            from there to bf16 (infinite past its largest value)
  * With res NULL, h is x itself and must be NULL here. The MXFP8 copy (q, s),
  * bf16 with d % 128 == 0 only, holds the rows of y exactly as moe_mx_quantize
  * axis 0 writes them from the rounded y: codes q [T,d], scales s of T*d/32
@@ -106,9 +107,9 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float
  * are not allowed.
  *
  * moe_add_rmsnorm_bwd: derived, its adjoint, with n = h * rs and g = dy * w:
- *   dx[t] = dh[t] + rs * (g - n * mean_i(g * n)), rounded once to `dtype`:
- *           the gradient of x and of res alike; dh (may be NULL) is what
- *           arrives at h along the residual
+ *   dx[t] = dh[t] + rs * (g - n * mean_i(g * n)), binary32 operations, their
+ *           result rounded to `dtype`: the gradient of x and of res alike; dh
+ *           (may be NULL) is what arrives at h along the residual
  *   dw    = sum_t dy[t] * n[t], binary32 sums in a fixed order, rounded once
  *           to `dtype`; dw may be NULL (a frozen w): then ws may be NULL too
  *   dy, h, dh, dx [T,d], w and dw [d] of `dtype`; rstd [T] from the forward;

@@ -86,27 +86,6 @@ template <int W, typename S> MOE_DEV S row_sum(S v, S* red, int wave) {
   return t;
 }
 
-// 1 / rms of a row, as 2^e * (hi + lo). A bf16 value h * rs * w is rounded to
-// binary32 once (h 2^e w is exact): with a binary32 sum of squares and two
-// rounded products 190 of 33 M stored values differed from the exactly rounded
-// ones and 12 of their 8-bit codes, with this and the sum in 64 bits 41 and 3,
-// for 0.6 us of 73.6.
-struct RowScale {
-  float value, unit, hi, lo;
-  MOE_DEV explicit RowScale(double r) : value(static_cast<float>(r)) {
-    int e = 0;
-    const double m = frexp(r, &e);
-    unit = ldexpf(1.f, e);
-    hi = static_cast<float>(m);
-    lo = static_cast<float>(m - hi);
-  }
-  template <typename T> MOE_DEV float times(float h, float w) const {
-    if constexpr (std::is_same<T, float>::value) return h * value * w;
-    const float p = h * unit * w;
-    return __builtin_fmaf(p, hi, p * lo);
-  }
-};
-
 template <int W> constexpr int kNormThreads = W == 1 ? 256 : 64 * W;   // four rows, or one
 
 // NT (launches that stream): x and res are read for the last time, h is next
@@ -159,16 +138,22 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
     sum += in ? sq : 0.0;
   }
   sum = row_sum<W>(sum, red, wave);
-  const RowScale rs(1.0 / sqrt(sum / d + a.eps));
-  if (a.rstd && c0 < min(nst, 1u)) a.rstd[t] = rs.value;
+  const double rs = 1.0 / sqrt(sum / d + a.eps);
+  if (a.rstd && c0 < min(nst, 1u)) a.rstd[t] = static_cast<float>(rs);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t c = c0 + 64 * W * u;
     float f[V], w[V];
     unpack(hv[u], f);
     unpack(wv[u], w);
+    // the product in 64 bits: y is rounded to binary32 once, and no factor of it
+    // leaves the range that y itself does not leave. Binary32 products with the
+    // root in two terms, which do, take 43.0 us where this takes 42.5 to 43.0
+    // (16384 x 2048 with a residual), 55.3 for 55.8 with the MXFP8 copy, 46.6 for
+    // 48.4 without a residual (32768 x 2048), 8.2 for 8.5 at 2048 rows
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = rs.times<T>(f[i], w[i]);
+    for (int i = 0; i < V; ++i)
+      f[i] = static_cast<float>(static_cast<double>(f[i]) * rs * static_cast<double>(w[i]));
     const V16 yv = pack(f);
     if (a.y && c < nst) store_piece<false>(static_cast<T*>(a.y) + t * d, c, yv);
     if constexpr (MX) {

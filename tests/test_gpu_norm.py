@@ -270,6 +270,15 @@ def test_permute_from_mx(T, d, k, E, cap):
 
 
 # ----------------------------------------------------------------------------- accuracy and range
+TOP = {"bf16": 2.0 ** 128 - 2.0 ** 119, "f32": 2.0 ** 128 - 2.0 ** 103}   # from here on a value rounds to infinity
+
+
+def half_step(v, kind):
+    """Half the distance of the storage type's neighbours around |v|."""
+    e = np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -126)))
+    return np.exp2(e - (8 if kind == "bf16" else 24))
+
+
 def run_forward(x, w, kind, eps):
     """(y, rstd) of the kernel and of the definition in 64 bits, at the eps it is given in binary32."""
     T, d = x.shape
@@ -286,10 +295,27 @@ def check_root(rstd, rs_ref):
 
 
 def check_rows(y, rstd, y_ref, rs_ref, kind):
-    """y takes half a step, the root's rounding (2 U where it is subnormal) and
-    two products' roundings."""
+    """y is the 64-bit product rounded to binary32 and, for bf16, from there to
+    the storage type: half a step of it, and half a step of binary32 before
+    that. Past the type's largest value it is infinite, with the sign."""
     check_root(rstd, rs_ref)
-    assert np.all(np.abs(y - y_ref) <= (STEP[kind] + 5 * U) * np.abs(y_ref) + 2.0 ** -133)
+    slack = U * (1 + 2.0 ** -10)
+    low = np.abs(y_ref) < TOP[kind] * (1 - 2 * U)
+    high = np.abs(y_ref) > TOP[kind] * (1 + 2 * U)
+    assert np.array_equal(y[high], np.copysign(np.inf, y_ref[high]))
+    tol = slack * np.abs(y_ref) if kind == "f32" else half_step(y_ref, kind) + slack * np.abs(y_ref)
+    assert np.all(np.abs(y - y_ref)[low] <= tol[low] + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(2048, 2048), (300, 2056), (64, 8200)])
+def test_stored_values_are_the_definitions_rounded(T, d, kind):
+    """Millions of values: a binary32 sum of squares, or a rounded product on
+    the way to y, leaves some of them past the bound."""
+    g = np.random.default_rng([13, T, d])
+    r = ROUND[kind]
+    x = r(g.standard_normal((T, d)) * np.where(g.random(d) < 0.02, 30.0, 1.0))
+    check_rows(*run_forward(x, r(1 + 0.2 * g.standard_normal(d)), kind, EPS), kind)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
@@ -306,6 +332,25 @@ def test_squares_past_binary32(d, kind):
     check_rows(*run_forward(same, w, kind, EPS), kind)
     check_rows(*run_forward(r(unit * np.array([[1e-19], [1e-20], [1e-21], [1e-22], [1e-25], [1.0]])), w, kind, 1e-40),
                kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [256, 1000, 2056])
+def test_products_at_the_end_of_the_range(d, kind):
+    """y near the type's largest value, past it (infinite with y's sign), and
+    finite behind a factor that is none of a normal number."""
+    g = np.random.default_rng([15, d])
+    r = ROUND[kind]
+    w = r(np.clip(g.standard_normal(d), -3, 3) * 1e38)
+    w[::4] = r(np.full(1, 3e38))
+    w[1::8] = r(np.full(1, 1e-38))
+    x = r(np.concatenate([np.full((1, d), 3.0), np.full((1, d), -0.7), g.standard_normal((40, d)), np.zeros((2, d))]))
+    x[-2, 5] = 7.0                                     # a spike: sqrt(d) * w
+    x[-1] = r(1e-3 * (1 + g.random(d)))                # beside 3e38 these are below 2^-126 before w
+    x[-1, 0] = r(np.full(1, 3e38))[0]
+    y, rstd, y_ref, rs_ref = run_forward(x, w, kind, EPS)
+    assert np.isinf(y).any() and np.isfinite(y[0]).all() and not np.isnan(y).any()
+    check_rows(y, rstd, y_ref, rs_ref, kind)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
