@@ -8,7 +8,8 @@ the expert layer, forward and backward.
             gradient of x and res (one tensor: they enter as a sum)
 
 With ``act8=True`` the norm writes n also as MXFP8 rows, which is all the layer
-keeps of it (see ``layer``): the bf16 n is released after the forward.
+keeps of it (see ``layer``; nothing where its MXFP8 experts alone read n): the
+bf16 n is released after the forward.
 
 Memory: h and the reciprocal roots stay from the forward to the backward. The
 buffers are allocated by the first pass and reused by later ones.
@@ -42,7 +43,7 @@ class MoEBlock:
         lay = self.layer
         if self.n is None:
             self.n = torch.empty(self.T, self.d, dtype=self.dtype, device=self.dev)
-        if lay.act8 and self.n8 is None:
+        if lay.reads_x8 and self.n8 is None:
             self.n8 = lay._rows8(self.T, self.d)
         if res is None:
             self.h = x
@@ -54,7 +55,7 @@ class MoEBlock:
         L.moe_add_rmsnorm(x, w_norm, self.eps, res=res, h=None if res is None else self.h, y=self.n, q=self.n8,
                           rstd=self.rstd)
         lay._mark("add_rmsnorm")
-        if lay.act8:
+        if lay.reads_x8:
             kw["x8"] = self.n8
         y = lay.forward(self.n, *weights, **kw)
         if lay.act8:

@@ -289,10 +289,16 @@ class MoELayer:
             self.x = None
         return self.y
 
+    @property
+    def reads_x8(self) -> bool:
+        """Whether the backward reads the input's 8-bit rows: not without act8,
+        nor where only the MXFP8 experts read the input, which hold their own
+        copy of the permuted rows."""
+        return self.act8 and not (self.mxfp8 and self.routing != "learned")
+
     def _keep_input(self, x, x8):
-        """The input's 8-bit rows, where the backward reads the input (the
-        MXFP8 experts hold their own copy of the permuted rows)."""
-        if self.mxfp8 and self.routing != "learned":
+        """The input's 8-bit rows, where the backward reads them."""
+        if not self.reads_x8:
             return
         if x8 is None:
             if self.x8 is None:

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from routing_grouped_expert_router_amd import _lib as L
+from routing_grouped_expert_router_amd.block import MoEBlock
 from routing_grouped_expert_router_amd.layer import MoELayer
 
 INVALID, UNSUPPORTED = -1, -2
@@ -129,3 +130,17 @@ def test_release_lets_go_of_the_mxfp8_experts_tensors_too(opts):
     lay.backward_buffers()
     assert lay.mx.y_perm is lay.y_perm and lay.mx.dx_perm is lay.dx_perm and lay.mx.dg is lay.dg
     assert (lay.mx.g8 is lay.g8 and lay.g8 is not None) if lay.act8 else lay.mx.g is lay.g
+
+
+@pytest.mark.parametrize("opts,reads", [(dict(), False), (dict(act8=True), True), (dict(act8=True, mxfp8=True), True),
+                                        (dict(act8=True, routing="given"), True),
+                                        (dict(act8=True, mxfp8=True, routing="given"), False)], ids=str)
+def test_block_writes_the_rows_its_layer_reads(opts, reads, monkeypatch):
+    """The norm writes the 8-bit rows only where the backward reads them."""
+    blk = MoEBlock(8, 256, 4, 2, 256, device="cpu", **opts)
+    seen = {}
+    monkeypatch.setattr(L, "moe_add_rmsnorm", lambda x, w, eps, **kw: seen.update(kw))
+    monkeypatch.setattr(blk.layer, "forward", lambda n, *a, **kw: seen.update(x8=kw.get("x8")))
+    x, w = torch.zeros(8, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
+    blk.forward(x, None, w)
+    assert (seen["q"] is not None) == (seen["x8"] is not None) == reads and seen["q"] is seen["x8"]

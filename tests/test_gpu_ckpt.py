@@ -383,3 +383,25 @@ def test_mxfp8_layer_releases_its_step(act8):
         left = torch.cuda.memory_allocated() - before
         assert left <= sum(v.numel() * v.element_size() for v in lay.grads().values()) + (1 << 20)
     assert peaks[1] <= peaks[0] and peaks[2] <= peaks[0]
+
+
+def test_block_of_mxfp8_experts_with_given_routing():
+    """No 8-bit rows of n are kept here: the layer's gradients are those of the
+    same layer called by itself."""
+    wl = workload("e128_uniform_bf16").scaled(**SMALL)
+    t = _inputs(wl)
+    kw = dict(topk_idx=t["topk_idx"], topk_w=t["topk_w"])
+    args, W = (t["w_gate"], t["w_up"], t["w_down"]), bf(np.linspace(0.5, 1.5, wl.d))
+    opts = dict(routing="given", mxfp8=True, act8=True)
+    blk, lay = MoEBlock(wl.T, wl.d, wl.E, wl.k, wl.F, **opts), MoELayer(wl.T, wl.d, wl.E, wl.k, wl.F, **opts)
+    n = torch.empty_like(t["x"])
+    L.moe_add_rmsnorm(t["x"], W, 1e-6, y=n)
+    for _ in range(2):
+        y, _ = blk.forward(t["x"], None, W, *args, **kw)
+        assert blk.n8 is None and torch.equal(y, lay.forward(n, *args, **kw))
+        dx, dn = blk.backward(t["dy"]), lay.backward(t["dy"])
+        for name, v in lay.grads().items():
+            assert torch.equal(v, blk.layer.grads()[name]), name
+        want, dw = torch.empty_like(dx), torch.empty_like(W)
+        L.moe_add_rmsnorm_bwd(dn, t["x"], W, blk.rstd, want, dw=dw, ws=blk.ws_norm)
+        assert torch.equal(dx, want) and torch.equal(blk.dw_norm, dw)
