@@ -104,7 +104,9 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_idx, float
  * binary32 (may be NULL) receives rs, rounded, for the backward pass.
  *   x, res, h, y [T,d] and w [d] of `dtype`; d <= MOE_MAX_NORM_D; eps > 0.
  * h and y may each be x or res itself (not both the same one); other overlaps
- * are not allowed.
+ * are not allowed. T up to 2^26 - 4, half of that where d takes two waves a row
+ * (over 2048 bf16 or 1024 binary32 values), and so on to twelve waves: more
+ * threads than one launch counts are MOE_ERR_UNSUPPORTED.
  *
  * moe_add_rmsnorm_bwd: derived, its adjoint, with n = h * rs and g = dy * w:
  *   dx[t] = dh[t] + rs * (g - n * mean_i(g * n)), binary32 operations, their
@@ -428,7 +430,8 @@ int moe_permute_mx(const void* x, int T, int d, int k, const int32_t* src_slot,
  * x_perm[row_of[s]] = deq(q[s / k]) for every kept slot s, and x = deq(q)
  * unless x is NULL, both from one read of the codes. src_slot as for
  * moe_permute.
- *   q, s: T rows of d, d % 128 == 0; x [T,d], x_perm [n_rows,d] bf16. */
+ *   q, s: T rows of d, d % 128 == 0; x [T,d], x_perm [n_rows,d] bf16.
+ * Both: fewer than 2^26 rows (else MOE_ERR_UNSUPPORTED). */
 int moe_mx_dequantize(const void* q, const void* s, int rows, int cols, void* dst, hipStream_t stream);
 int moe_permute_from_mx(const void* q, const void* s, int T, int d, int k, const int32_t* row_of,
                         const int32_t* src_slot, int n_rows, void* x, void* x_perm, hipStream_t stream);

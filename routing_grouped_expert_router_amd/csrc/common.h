@@ -130,6 +130,9 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 inline bool valid_dtype(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 inline size_t dtype_bytes(int dt) { return dt == MOE_F32 ? 4 : 2; }
 
+// A launch's threads are counted in 32 bits: more blocks than this are refused.
+inline bool launchable(long blocks, int threads) { return blocks * threads < (1L << 32); }
+
 inline int launch_status() {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

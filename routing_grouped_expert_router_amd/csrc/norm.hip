@@ -370,14 +370,18 @@ template <typename T> int norm_bwd_grid(int T_, int waves) {
   return static_cast<int>((T_ + per - 1) / per);
 }
 
-template <typename T, bool MX> void launch_norm(const NormArgs& a, hipStream_t s) {
+template <typename T, bool MX> int launch_norm(const NormArgs& a, hipStream_t s) {
   const bool stream = (long)a.T * a.d * sizeof(T) * (a.res ? 4 : 2) >= kStreamBytes;
+  bool ok = true;
   norm_shape<T>(a.d, [&](auto w, auto u) {
     constexpr int W = w(), U = u();
     const int grid = W == 1 ? static_cast<int>((a.T + 3L) / 4) : a.T;
+    if (!(ok = launchable(grid, kNormThreads<W>))) return;
     if (stream) add_rmsnorm_kernel<T, W, U, MX, true><<<grid, kNormThreads<W>, 0, s>>>(a);
     else add_rmsnorm_kernel<T, W, U, MX, false><<<grid, kNormThreads<W>, 0, s>>>(a);
   });
+  MOE_CHECK_SUPPORTED(ok);
+  return launch_status();
 }
 
 template <typename T> int launch_norm_bwd(const NormBwdArgs& a, void* dw, hipStream_t s) {
@@ -412,10 +416,8 @@ extern "C" int moe_add_rmsnorm(int dtype, const void* x, const void* res, const 
   MOE_CHECK_ARG(x && w && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(h) && aligned16(y));
   MOE_CHECK_ARG(aligned16(q) && aligned4(s) && aligned4(rstd));
   const NormArgs a{x, res, w, h, y, static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), rstd, T, d, eps};
-  if (dtype == MOE_F32) launch_norm<float, false>(a, stream);
-  else if (q) launch_norm<uint16_t, true>(a, stream);
-  else launch_norm<uint16_t, false>(a, stream);
-  return launch_status();
+  if (dtype == MOE_F32) return launch_norm<float, false>(a, stream);
+  return q ? launch_norm<uint16_t, true>(a, stream) : launch_norm<uint16_t, false>(a, stream);
 }
 
 extern "C" size_t moe_add_rmsnorm_bwd_workspace_bytes(int T, int d) {

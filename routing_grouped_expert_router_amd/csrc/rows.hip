@@ -490,6 +490,7 @@ extern "C" int moe_permute_from_mx(const void* q, const void* s, int T, int d, i
   MOE_CHECK_ARG(d % 128 == 0 && (src_slot || (long)n_rows == (long)T * k));
   MOE_CHECK_ARG(T == 0 || (q && s && row_of && aligned16(q) && aligned4(s) && aligned16(x)));
   MOE_CHECK_ARG(n_rows == 0 || (x_perm && aligned16(x_perm)));
+  MOE_CHECK_SUPPORTED(launchable(row_grid(T), kRowThreads) && (!src_slot || launchable(row_grid(n_rows), kRowThreads)));
   if (src_slot)
     if (int st = zero_pads<uint16_t>(src_slot, n_rows, d, x_perm, stream)) return st;
   if (T == 0) return MOE_OK;
@@ -500,6 +501,7 @@ extern "C" int moe_mx_dequantize(const void* q, const void* s, int rows, int col
   MOE_CHECK_ARG(rows >= 0 && cols > 0 && cols % 128 == 0);
   if (rows == 0) return MOE_OK;
   MOE_CHECK_ARG(q && s && dst && aligned16(q) && aligned4(s) && aligned16(dst));
+  MOE_CHECK_SUPPORTED(launchable(row_grid(rows), kRowThreads));
   return launch_from_mx(q, s, rows, cols, 0, nullptr, 0, dst, nullptr, stream);
 }
 

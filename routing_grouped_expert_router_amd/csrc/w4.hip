@@ -558,7 +558,6 @@ template <bool GATE_UP> int launch_w4(const W4Args& a, hipStream_t s) {
   const int chunks = (K / kStepK + kChunk - 1) / kChunk;
   const int wk = chunks >= 3 ? 4 : chunks;   // waves that share a tile's K: as many as it has chunks, up to 4
   const long units = min(R, a.E);
-  MOE_CHECK_SUPPORTED(units * tiles < (1L << 31));
   auto groups_of = [&](int nt) { return (tiles + 4 * nt - 1) / (4 * nt); };
   const int few = !GATE_UP ? kFewRowsDown : units * groups_of(1) >= 512 ? kFewRows : kFewRowsSmall;
   if (R <= few * a.E) {
@@ -609,7 +608,7 @@ extern "C" int moe_w4_quantize(const void* w, int n_mat, int K, int N, void* q, 
   MOE_CHECK_ARG(w && q && s && aligned16(w) && aligned16(q) && aligned4(s));
   const int tiles_c = (N + kQuantCols - 1) / kQuantCols;
   const long grid = (long)n_mat * tiles_c * (K / kStepK);
-  MOE_CHECK_SUPPORTED(grid < (1L << 31));
+  MOE_CHECK_SUPPORTED(launchable(grid, kW4Threads));
   w4_quantize_kernel<<<(int)grid, kW4Threads, 0, stream>>>(static_cast<const uint16_t*>(w), K, N, tiles_c,
                                                           static_cast<uint8_t*>(q), static_cast<uint8_t*>(s));
   return launch_status();
@@ -625,6 +624,11 @@ extern "C" int moe_experts_w4(const moe_w4_desc* g, hipStream_t stream) {
   MOE_CHECK_ARG(g->T >= 0 && g->d > 0 && g->F > 0 && g->E >= 1 && g->k >= 1 && g->d % kStepK == 0 && g->F % kStepK == 0);
   MOE_CHECK_SUPPORTED(g->E <= MOE_MAX_EXPERTS && g->k <= MOE_MAX_TOPK && (long)g->T * g->k <= MOE_W4_MAX_SLOTS);
   if (g->T == 0) return MOE_OK;
+  // refused before anything is launched: no kernel takes more workgroups than
+  // one for each 16 columns of each expert (or slot); the sum, a thread for four columns
+  const long slots = (long)g->T * g->k, units = slots < g->E ? slots : g->E, cols = g->d > g->F ? g->d : g->F;
+  MOE_CHECK_SUPPORTED(launchable(units * (cols / kTileN), 64 * kOneWaves));
+  MOE_CHECK_SUPPORTED(launchable(((long)g->T * (g->d / 4) + 255) / 256, 256));
   MOE_CHECK_ARG(g->x && g->topk_idx && g->topk_w && g->y && aligned16(g->x) && aligned16(g->y) && aligned16(g->y_add));
   MOE_CHECK_ARG(aligned4(g->topk_idx) && aligned4(g->topk_w));
   for (const moe_w4_tensor* w : {&g->w_gate, &g->w_up, &g->w_down})

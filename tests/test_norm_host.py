@@ -114,3 +114,24 @@ def test_binding_refuses_mismatched_tensors():
         L.moe_permute_from_mx(mx, 2, rows, None, torch.empty(10, 256, dtype=bf))
     with pytest.raises(L.MoEError, match="x: shape"):
         L.moe_permute_from_mx(mx, 2, rows[:8], None, torch.empty(8, 256, dtype=bf), x=torch.empty(4, 128, dtype=bf))
+
+
+def test_rows_past_one_launch_are_refused():
+    """A launch counts its threads in 32 bits: 64 for each row of a wave."""
+    lib = L.lib()
+    A = [0x1000 * i for i in range(1, 12)]
+
+    def norm(dtype, T, d, mx=False):
+        return lib.moe_add_rmsnorm(dtype, A[0], A[1], A[2], T, d, 1e-6, A[3], A[4], A[5] if mx else None,
+                                   A[6] if mx else None, A[7], None)
+
+    assert norm(1, 1 << 26, 8) == UNSUPPORTED and norm(0, 1 << 26, 8) == UNSUPPORTED
+    assert norm(1, 1 << 26, 128, True) == UNSUPPORTED and norm(1, (1 << 31) - 1, 2048) == UNSUPPORTED
+    assert norm(1, 1 << 25, 2056) == UNSUPPORTED and norm(0, 1 << 25, 1032) == UNSUPPORTED     # two waves a row
+    assert norm(1, 1 << 24, 8192) == UNSUPPORTED and norm(0, 5592406, 12288) == UNSUPPORTED    # four, twelve
+    f = lib.moe_permute_from_mx
+    assert f(A[0], A[1], 1 << 26, 128, 1, A[2], None, 1 << 26, A[3], A[4], None) == UNSUPPORTED
+    assert f(A[0], A[1], 8, 128, 1, A[2], A[5], 1 << 26, A[3], A[4], None) == UNSUPPORTED      # pad rows
+    assert f(A[0], A[1], (1 << 31) - 1, 128, 1, A[2], None, (1 << 31) - 1, A[3], A[4], None) == UNSUPPORTED
+    assert lib.moe_mx_dequantize(A[0], A[1], 1 << 26, 128, A[2], None) == UNSUPPORTED
+    assert lib.moe_mx_dequantize(A[0], A[1], (1 << 31) - 1, 128, A[2], None) == UNSUPPORTED

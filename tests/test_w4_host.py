@@ -97,3 +97,14 @@ def test_binding_refuses_mismatched_tensors():
 def test_decoder_refuses_batches_past_the_slot_limit():
     with pytest.raises(ValueError, match="4096"):
         MoEDecoder(None, None, torch.empty(8, 128, 128), None, None, k=4, max_tokens=1025)
+
+
+def test_widths_past_one_launch_are_refused():
+    """A launch counts its threads in 32 bits."""
+    lib = L.lib()
+    need = 1 << 40
+    call = lambda **kw: lib.moe_experts_w4(C.byref(desc(ws_bytes=need, **kw)), None)
+    assert call(T=1024, k=1, E=1024, F=1 << 20) == UNSUPPORTED            # 1024 experts of 65536 tiles
+    assert call(T=1024, k=1, E=1024, d=1 << 20) == UNSUPPORTED
+    assert call(T=4096, k=1, E=1, d=1 << 22) == UNSUPPORTED               # the weighted sum's threads
+    assert lib.moe_w4_quantize(FAKE, 1 << 14, 1 << 14, 1 << 9, FAKE, FAKE, None) == UNSUPPORTED
