@@ -284,6 +284,13 @@ def moe_route(logits, k, topk_idx, topk_w, stream=None):
 
 
 # ----------------------------------------------------------------- norm
+def _rows(T: int) -> int:
+    """T where the library takes an int, which ctypes would fill with its low 32 bits."""
+    if T > 0x7FFFFFFF:
+        raise MoEError(f"{T} rows, at most {0x7FFFFFFF}")
+    return T
+
+
 def moe_add_rmsnorm(x, w, eps, res=None, h=None, y=None, q: Optional[MxTensor] = None, rstd=None, stream=None):
     dt, shape = x.dtype, x.shape
     T, d = shape
@@ -295,12 +302,12 @@ def moe_add_rmsnorm(x, w, eps, res=None, h=None, y=None, q: Optional[MxTensor] =
         scales = _req(q.s, "q.s", torch.uint8, min_numel=T * d // 32)
         _same_device(x, w, res, h, y, rstd, q.q, q.s)
     _call("moe_add_rmsnorm", _dt(x), _req(x, "x", dt, shape), _req(res, "res", dt, shape, True),
-          _req(w, "w", dt, (d,)), T, d, eps, _req(h, "h", dt, shape, True), _req(y, "y", dt, shape, True),
+          _req(w, "w", dt, (d,)), _rows(T), d, eps, _req(h, "h", dt, shape, True), _req(y, "y", dt, shape, True),
           codes, scales, _req(rstd, "rstd", torch.float32, (T,), True), _stream(stream))
 
 
 def moe_add_rmsnorm_bwd_workspace_bytes(T, d) -> int:
-    return lib().moe_add_rmsnorm_bwd_workspace_bytes(T, d)
+    return lib().moe_add_rmsnorm_bwd_workspace_bytes(_rows(T), d)
 
 
 def moe_add_rmsnorm_bwd(dy, h, w, rstd, dx, dw=None, dh=None, ws=None, stream=None):
@@ -309,7 +316,7 @@ def moe_add_rmsnorm_bwd(dy, h, w, rstd, dx, dw=None, dh=None, ws=None, stream=No
     _same_device(dy, h, w, rstd, dx, dw, dh, ws)
     _call("moe_add_rmsnorm_bwd", _dt(dy), _req(dy, "dy", dt, (T, d)), _req(h, "h", dt, (T, d)),
           _req(w, "w", dt, (d,)), _req(rstd, "rstd", torch.float32, (T,)), _req(dh, "dh", dt, (T, d), optional=True),
-          T, d, _req(dx, "dx", dt, (T, d)), _req(dw, "dw", dt, (d,), optional=True), _p(ws),
+          _rows(T), d, _req(dx, "dx", dt, (T, d)), _req(dw, "dw", dt, (d,), optional=True), _p(ws),
           0 if ws is None else _nbytes(ws), _stream(stream))
 
 

@@ -135,3 +135,15 @@ def test_rows_past_one_launch_are_refused():
     assert f(A[0], A[1], (1 << 31) - 1, 128, 1, A[2], None, (1 << 31) - 1, A[3], A[4], None) == UNSUPPORTED
     assert lib.moe_mx_dequantize(A[0], A[1], 1 << 26, 128, A[2], None) == UNSUPPORTED
     assert lib.moe_mx_dequantize(A[0], A[1], (1 << 31) - 1, 128, A[2], None) == UNSUPPORTED
+
+
+def test_binding_refuses_row_counts_past_32_bits():
+    """2^32 + 4 rows are not 4: a row count is an int of the library's."""
+    T, bf = (1 << 32) + 4, torch.bfloat16
+    x, w = torch.empty(T, 8, dtype=bf, device="meta"), torch.ones(8, dtype=bf)
+    with pytest.raises(L.MoEError, match="rows"):
+        L.moe_add_rmsnorm(x, w, 1e-6, y=x)
+    with pytest.raises(L.MoEError, match="rows"):
+        L.moe_add_rmsnorm_bwd(x, x, w, torch.empty(T, device="meta"), x, dw=w)
+    with pytest.raises(L.MoEError, match="rows"):
+        L.moe_add_rmsnorm_bwd_workspace_bytes(T, 8)
