@@ -427,6 +427,7 @@ _GG_NUMEL = {
 def make_gg_desc(op, dtype, E, d, F, n_rows, capacity=0, group_offsets=None, ws=None,
                  **tensors) -> moe_gg_desc:
     desc = moe_gg_desc(op, dtype, E, d, F, n_rows, capacity)
+    desc.tensors = (group_offsets, ws, *tensors.values())
     fields = [((desc, "group_offsets"), _req(group_offsets, "group_offsets", torch.int32, E + 1, optional=True))]
     tdt = torch.bfloat16 if dtype == MOE_BF16 else torch.float32
     for name, t in tensors.items():
@@ -453,6 +454,9 @@ def _ckpt(desc, g: MxTensor, u: MxTensor):
     """The 8-bit rows of G and U as descriptors, checked against desc's sizes."""
     n, u8 = desc.n_rows * desc.F, torch.uint8
     _same_device(g.q, g.s, u.q, u.s)
+    if not _one_device:
+        for t in getattr(desc, "tensors", ()):
+            _same_device(*((t.q, t.s) if isinstance(t, MxTensor) else (t,)))
     at = (_req(g.q, "g.q", u8, min_numel=n), _req(g.s, "g.s", u8, min_numel=n // 32),
           _req(u.q, "u.q", u8, min_numel=n), _req(u.s, "u.s", u8, min_numel=n // 32))
     if _HOST in at:
@@ -523,6 +527,7 @@ def make_mx_gg_desc(op, E, d, F, n_rows, group_offsets, col_stride=0, a0=None, a
                     b1=None, g=None, u=None, out0=None, out1=None, out2=None, ws=None, qo0_rows=None,
                     qo0_cols=None, qo1_rows=None, qo1_cols=None) -> moe_mx_gg_desc:
     desc = moe_mx_gg_desc()
+    desc.tensors = (group_offsets, a0, a1, b0, b1, g, u, out0, out1, out2, ws, qo0_rows, qo0_cols, qo1_rows, qo1_cols)
     desc.op, desc.E, desc.d, desc.F, desc.n_rows, desc.col_stride = op, E, d, F, n_rows, col_stride
     fields = [((desc, "group_offsets"), _req(group_offsets, "group_offsets", torch.int32, E + 1, optional=True))]
     for name, t in (("a0", a0), ("a1", a1), ("b0", b0), ("b1", b1), ("qo0_rows", qo0_rows),

@@ -144,3 +144,46 @@ def test_block_writes_the_rows_its_layer_reads(opts, reads, monkeypatch):
     x, w = torch.zeros(8, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
     blk.forward(x, None, w)
     assert (seen["q"] is not None) == (seen["x8"] is not None) == reads and seen["q"] is seen["x8"]
+
+
+class OnDevice:
+    """What the binding asks of a contiguous device tensor; never dereferenced."""
+
+    def __init__(self, dtype, shape, at):
+        self.dtype, self.shape, self.is_cuda, self.at = dtype, shape, True, at
+
+    numel = lambda self: int(torch.tensor(self.shape).prod())
+    element_size = lambda self: self.dtype.itemsize
+    is_contiguous = lambda self: True
+    data_ptr = lambda self: FAKE
+    get_device = lambda self: self.at
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("name", [None, "x", "w", "offsets", "copy"])
+def test_every_tensor_has_to_be_on_the_current_device(mx, name, monkeypatch):
+    monkeypatch.setattr(L, "_one_device", False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(L, "_stream", lambda s=None: None)
+    called = []
+    monkeypatch.setattr(L, "_call", lambda f, *a: called.append(f))
+    at = lambda n: 1 if n == name else 0
+    t = lambda n, *shape, dtype=torch.bfloat16: OnDevice(dtype, shape, at(n))
+    q = lambda n, rows, cols: L.MxTensor(t(n, rows, cols, dtype=torch.uint8), t(n, rows * cols // 32, dtype=torch.uint8))
+    off = t("offsets", 5, dtype=torch.int32)
+    if mx:
+        desc = L.make_mx_gg_desc(L.MOE_GG_FWD_GATE_UP, 4, 256, 256, 64, off, a0=q("x", 64, 256), b0=q("w", 256, 1024),
+                                 b1=q("w", 256, 1024), out2=t("h", 64, 256))
+        call = L.moe_grouped_gemm_mx_ckpt
+    else:
+        desc = L.make_gg_desc(L.MOE_GG_FWD_GATE_UP, L.MOE_BF16, 4, 256, 256, 64, 0, off, x_perm=t("x", 64, 256),
+                              w_gate=t("w", 4, 256, 256), w_up=t("w", 4, 256, 256), h=t("h", 64, 256))
+        call = L.moe_grouped_gemm_ckpt
+    copies = q("copy", 64, 256), q("other copy", 64, 256)
+    if name is None:
+        call(desc, *copies)
+        assert called == [call.__name__]
+    else:
+        with pytest.raises(L.MoEError, match="on cuda:1, the current device is cuda:0"):
+            call(desc, *copies)
+        assert called == []
