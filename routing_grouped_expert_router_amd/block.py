@@ -45,12 +45,14 @@ class MoEBlock:
             self.n = torch.empty(self.T, self.d, dtype=self.dtype, device=self.dev)
         if lay.reads_x8 and self.n8 is None:
             self.n8 = lay._rows8(self.T, self.d)
-        if res is None:
+        # the layer writes over its own last y: as x without res it is copied first
+        own = res is None and lay.y is not None and x.data_ptr() == lay.y.data_ptr()
+        if res is None and not own:
             self.h = x
         else:
             if self._sum is None:
                 self._sum = torch.empty(self.T, self.d, dtype=self.dtype, device=self.dev)
-            self.h = self._sum
+            self.h = self._sum.copy_(x) if own else self._sum
         self.w_norm = w_norm
         L.moe_add_rmsnorm(x, w_norm, self.eps, res=res, h=None if res is None else self.h, y=self.n, q=self.n8,
                           rstd=self.rstd)

@@ -405,3 +405,22 @@ def test_block_of_mxfp8_experts_with_given_routing():
         want, dw = torch.empty_like(dx), torch.empty_like(W)
         L.moe_add_rmsnorm_bwd(dn, t["x"], W, blk.rstd, want, dw=dw, ws=blk.ws_norm)
         assert torch.equal(dx, want) and torch.equal(blk.dw_norm, dw)
+
+
+@pytest.mark.parametrize("act8", [False, True])
+def test_block_fed_its_own_output_without_a_residual(act8):
+    """x is the block's own y buffer, which the pass writes: h, which is x then,
+    must still be x when the backward reads it."""
+    wl = workload("e128_uniform_bf16").scaled(T=33, d=256, F=256, E=8)
+    t = _inputs(wl)
+    kw = dict(topk_idx=t["topk_idx"], topk_w=t["topk_w"])
+    args, W = (t["w_gate"], t["w_up"], t["w_down"]), bf(np.linspace(0.5, 1.5, wl.d))
+    mk = lambda: MoEBlock(wl.T, wl.d, wl.E, wl.k, wl.F, routing="given", act8=act8)
+    a, b = mk(), mk()
+    y, _ = a.forward(t["x"], None, W, *args, **kw)
+    x = y.clone()
+    y_a, h_a = a.forward(y, None, W, *args, **kw)
+    y_b, h_b = b.forward(x, None, W, *args, **kw)
+    assert torch.equal(y_a, y_b) and torch.equal(h_a, x) and h_b is x
+    dx_a, dx_b = a.backward(t["dy"]), b.backward(t["dy"])
+    assert torch.equal(dx_a, dx_b) and torch.equal(a.dw_norm, b.dw_norm)
