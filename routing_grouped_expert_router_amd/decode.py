@@ -24,6 +24,10 @@ def quantize_experts(w: torch.Tensor) -> L.W4Tensor:
     return out
 
 
+def _lies_in(v: torch.Tensor, buf: torch.Tensor) -> bool:
+    return 0 <= v.data_ptr() - buf.data_ptr() < buf.numel() * buf.element_size()
+
+
 class MoEDecoder:
     def __init__(self, w_norm, w_r, w_gate, w_up, w_down, k: int, max_tokens: int, eps: float = 1e-6,
                  w_gate_s=None, w_up_s=None, w_down_s=None):
@@ -52,13 +56,19 @@ class MoEDecoder:
     def step(self, x, res=None):
         """x and res [T, d] bf16, T <= max_tokens (res None: the first block).
         Returns (y, h), views of this decoder's buffers (h is x itself without
-        res), overwritten by the next step."""
+        res), overwritten by the next step. y may come back as x: without res it
+        is copied first."""
         T = x.shape[0]
         if T > self.T:
             raise ValueError(f"{T} tokens, made for {self.T}")
         if T == 0:
             return self.y[:0], x if res is None else self.h[:0]
-        n, y, h = self.n[:T], self.y[:T], x if res is None else self.h[:T]
+        n, y, h = self.n[:T], self.y[:T], self.h[:T]
+        if res is None:
+            if _lies_in(x, self.y):      # what is returned as h
+                h.copy_(x)
+            else:
+                h = x
         L.moe_add_rmsnorm(x, self.w_norm, self.eps, res=res, h=None if res is None else h, y=n)
         logits, idx, p = self.logits[:T], self.topk_idx[:T], self.topk_w[:T]
         L.moe_router_gemm(n, self.w_r, logits)

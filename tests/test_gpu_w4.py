@@ -291,3 +291,44 @@ def test_decode_on_another_stream():
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_decode_step_fed_its_own_output_without_a_residual(shared):
+    """x is the decoder's own y, which the step writes: the h it returns is still x."""
+    dec, _, _, g = decoder(shared)
+    other, _, _, _ = decoder(shared)
+    y, _ = dec.step(bf(g.standard_normal((5, 256))))
+    x = y.clone()
+    y1, h1 = dec.step(y)
+    y2, h2 = other.step(x)
+    assert torch.equal(y1, y2) and torch.equal(h1, x) and h2 is x
+    z = y1.clone()
+    y1, h1 = dec.step(y1[1:3])                                   # some of its rows
+    assert torch.equal(h1, z[1:3])
+    y1, h1 = dec.step(y1, h1)
+    y2, h2 = other.step(z[1:3].clone())
+    y2, h2 = other.step(y2.clone(), h2)
+    assert torch.equal(y1, y2) and torch.equal(h1, h2)
+
+
+def test_decode_step_without_a_residual_captured():
+    """The copy of an own output inside a graph, replayed beside eager steps."""
+    dec, _, _, g = decoder(True)
+    eager, _, _, _ = decoder(True)
+    x = bf(g.standard_normal((3, 256)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        dec.step(dec.step(x)[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = dec.step(dec.step(x)[0])
+    for i in range(4):
+        x.copy_(torch.roll(x, 1, 1))
+        first = eager.step(x)[0].clone()
+        want = eager.step(first)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(h, first), i
