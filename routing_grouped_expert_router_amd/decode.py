@@ -56,8 +56,9 @@ class MoEDecoder:
     def step(self, x, res=None):
         """x and res [T, d] bf16, T <= max_tokens (res None: the first block).
         Returns (y, h), views of this decoder's buffers (h is x itself without
-        res), overwritten by the next step. y may come back as x: without res it
-        is copied first."""
+        res), overwritten by the next step. They, and rows of them, may come
+        back as x and res: a view that the step would overwrite before it is
+        done with it is copied first."""
         T = x.shape[0]
         if T > self.T:
             raise ValueError(f"{T} tokens, made for {self.T}")
@@ -69,6 +70,8 @@ class MoEDecoder:
                 h.copy_(x)
             else:
                 h = x
+        else:                            # the rows of h in another place than they are read from
+            x, res = (v.clone() if _lies_in(v, self.h) and v.data_ptr() != h.data_ptr() else v for v in (x, res))
         L.moe_add_rmsnorm(x, self.w_norm, self.eps, res=res, h=None if res is None else h, y=n)
         logits, idx, p = self.logits[:T], self.topk_idx[:T], self.topk_w[:T]
         L.moe_router_gemm(n, self.w_r, logits)

@@ -312,6 +312,21 @@ def test_decode_step_fed_its_own_output_without_a_residual(shared):
     assert torch.equal(y1, y2) and torch.equal(h1, h2)
 
 
+@pytest.mark.parametrize("rows", [slice(0, 12), slice(1, 20), slice(7, 8)], ids=str)
+def test_decode_step_fed_rows_of_its_own_output(rows):
+    """Sequences that end leave a batch: the rows that stay are read from where
+    other rows' h goes."""
+    dec, _, _, g = decoder(False)
+    other, _, _, _ = decoder(False)
+    x, res = bf(g.standard_normal((20, 256))), bf(g.standard_normal((20, 256)))
+    y, h = dec.step(x, res)
+    want = other.step(y[rows].clone(), h[rows].clone())
+    want = other.step(want[1].clone(), want[0].clone())
+    got = dec.step(y[rows], h[rows])
+    got = dec.step(got[1], got[0])                               # h as x: its own rows again
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_decode_step_without_a_residual_captured():
     """The copy of an own output inside a graph, replayed beside eager steps."""
     dec, _, _, g = decoder(True)

@@ -108,3 +108,27 @@ def test_widths_past_one_launch_are_refused():
     assert call(T=1024, k=1, E=1024, d=1 << 20) == UNSUPPORTED
     assert call(T=4096, k=1, E=1, d=1 << 22) == UNSUPPORTED               # the weighted sum's threads
     assert lib.moe_w4_quantize(FAKE, 1 << 14, 1 << 14, 1 << 9, FAKE, FAKE, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows", [slice(0, 3), slice(1, 4), slice(4, 5)], ids=str)
+@pytest.mark.parametrize("swap", [False, True])
+def test_decoder_hands_the_norm_no_rows_that_it_overwrites(rows, swap, monkeypatch):
+    """Rows of the decoder's own h may come back as res (or x): the norm may
+    write h over them only where each row is its own."""
+    monkeypatch.setattr(L, "moe_w4_quantize", lambda w, out: None)
+    b = lambda *s: torch.randn(*s).to(torch.bfloat16)
+    dec = MoEDecoder(b(128), b(128, 4), b(4, 128, 128), b(4, 128, 128), b(4, 128, 128), k=2, max_tokens=5)
+    for name in ("moe_router_gemm", "moe_route", "moe_experts_w4"):
+        monkeypatch.setattr(L, name, lambda *a, **kw: None)
+    calls = []
+    monkeypatch.setattr(L, "moe_add_rmsnorm", lambda x, w, eps, **kw: calls.append((x, kw["res"], kw["h"])))
+    x, res = dec.y[rows], dec.h[rows]
+    x.copy_(b(*x.shape))
+    res.copy_(b(*res.shape))
+    want = (res.clone(), x.clone()) if swap else (x.clone(), res.clone())
+    dec.step(*((res, x) if swap else (x, res)))
+    (gx, gres, h), = calls
+    assert torch.equal(gx, want[0]) and torch.equal(gres, want[1])
+    size = h.numel() * h.element_size()
+    for t in (gx, gres):
+        assert t.data_ptr() == h.data_ptr() or abs(t.data_ptr() - h.data_ptr()) >= size
