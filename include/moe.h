@@ -64,7 +64,10 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 /* Text for a status code (static storage; never NULL). */
 const char* moe_status_string(int status);
 
-/* ABI version of this header: 6. */
+/* ABI version of this header: 6, that of the entry points and structures up to
+ * moe_grouped_gemm_mx. The norm, the checkpoint and the 4-bit experts were added
+ * without a change to those and without a new number: a library that lacks
+ * them is told by its missing symbols. */
 int moe_abi_version(void);
 
 /* ----------------------------------------------------------------- router

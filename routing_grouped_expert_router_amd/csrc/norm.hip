@@ -8,9 +8,9 @@
 // Memory-bound in both directions: every element is read and written once, and
 // a whole row stays in the registers of the 1 to 12 waves that share it, so
 // the norm and the quantisation cost no second pass. 16384 x 2048 bf16 with a
-// residual: forward 42.9 us (6.3 TB/s; a plain copy reaches 5.1), 51 to 56
-// with the MXFP8 copy, backward 48.3 us with dw; one token 3.0 us, 2.7 of them a
-// launch's own. See include/moe.h for the contract of each entry point.
+// residual: forward 42.7 us (6.3 TB/s; a plain copy reaches 5.1), 51 to 57
+// with the MXFP8 copy, in binary32 92 us (5.8 TB/s), backward 48.3 us with dw; one
+// token 3.0 us, 2.7 of them a launch's own. See include/moe.h for the contract of each entry point.
 #include "mx_common.h"
 
 #include <type_traits>
@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
       unpack(hv[u], f);
       if (c0 + 64 * W * u < nst) store_piece<NT>(static_cast<T*>(a.h) + t * d, c0 + 64 * W * u, hv[u]);
     }
-    // every square and every sum in 64 bits (43.1 us of the large batch against
-    // 43.3, so: nothing): in binary32 a square of 2e19 is infinite already
+    // every square and every sum in 64 bits (16384 x 2048 43.3 us, with groups of
+    // eight squares added in binary32 43.1): a square of 2e19 is infinite there
     double sq = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) sq = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), sq);
@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kNormThreads<W>) add_rmsnorm_kernel(NormArgs a
     unpack(hv[u], f);
     unpack(wv[u], w);
     // the product in 64 bits: y is rounded to binary32 once, and no factor of it
-    // leaves the range that y itself does not leave. Binary32 products with the
-    // root in two terms, which do, take 43.0 us where this takes 42.5 to 43.0
+    // leaves the range that y itself does not leave (all of 33 M bf16 values are
+    // the exact ones rounded by way of binary32). Binary32 products with the root
+    // in two terms, which do leave it, take 43.0 us where this takes 42.5 to 43.0
     // (16384 x 2048 with a residual), 55.3 for 55.8 with the MXFP8 copy, 46.6 for
     // 48.4 without a residual (32768 x 2048), 8.2 for 8.5 at 2048 rows
 #pragma unroll

@@ -6,8 +6,10 @@
 
 for one token up to ``max_tokens``, which times k is at most
 MOE_W4_MAX_SLOTS. The expert weights are quantised once, here; the bf16 ones
-are not kept. Seven launches (two or three more with a shared expert), no host
-synchronisation and no allocation in a step, so a step can be captured into a
+are not kept. Five launches for a token (norm, router GEMM, top-k, gate/up, down
+with the sum), six for a batch (the sum by itself), two or three more with a
+shared expert; no host synchronisation, and no allocation unless rows of an
+earlier step's h come back in another place, so a step can be captured into a
 graph; a graph then owns this decoder's buffers.
 """
 from __future__ import annotations
