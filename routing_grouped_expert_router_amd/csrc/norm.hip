@@ -409,11 +409,11 @@ extern "C" int moe_add_rmsnorm(int dtype, const void* x, const void* res, const 
                                void* h, void* y, void* q, void* s, float* rstd, hipStream_t stream) {
   MOE_CHECK_ARG(valid_dtype(dtype) && T >= 0 && d > 0 && d % 8 == 0);
   MOE_CHECK_ARG(eps > 0.0f && eps < INFINITY);
+  MOE_CHECK_SUPPORTED(d <= MOE_MAX_NORM_D);
+  if (T == 0) return MOE_OK;   // tensors of no row may have no address
   MOE_CHECK_ARG((q == nullptr) == (s == nullptr) && (res == nullptr) == (h == nullptr));
   MOE_CHECK_ARG(q == nullptr || (dtype == MOE_BF16 && d % 128 == 0));
   MOE_CHECK_ARG(y != nullptr || q != nullptr);
-  MOE_CHECK_SUPPORTED(d <= MOE_MAX_NORM_D);
-  if (T == 0) return MOE_OK;
   MOE_CHECK_ARG(x && w && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(h) && aligned16(y));
   MOE_CHECK_ARG(aligned16(q) && aligned4(s) && aligned4(rstd));
   const NormArgs a{x, res, w, h, y, static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), rstd, T, d, eps};

@@ -425,3 +425,24 @@ def test_block_fed_its_own_output_without_a_residual(act8):
     assert torch.equal(y_a, y_b) and torch.equal(h_a, x) and h_b is x
     dx_a, dx_b = a.backward(t["dy"]), b.backward(t["dy"])
     assert torch.equal(dx_a, dx_b) and torch.equal(a.dw_norm, b.dw_norm)
+
+
+@pytest.mark.parametrize("opts", [{}, dict(act8=True), dict(act8=True, mxfp8=True), dict(act8=True, capacity=8),
+                                  dict(act8=True, shared_ff=256)], ids=str)
+def test_block_without_tokens(opts):
+    """A rank that is given no token: empty outputs, and gradients of zero."""
+    d, E, k, F = 256, 4, 2, 256
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF) * 0.05
+    kw = {}
+    if "shared_ff" in opts:
+        kw = dict(w_gate_s=rand(d, 256), w_up_s=rand(d, 256), w_down_s=rand(256, d))
+    blk = MoEBlock(0, d, E, k, F, routing="given", **opts)
+    e = torch.empty(0, d, dtype=BF, device="cuda")
+    idx, p = torch.empty(0, k, dtype=torch.int32, device="cuda"), torch.empty(0, k, device="cuda")
+    y, h = blk.forward(e, e.clone(), rand(d), rand(E, d, F), rand(E, d, F), rand(E, F, d), topk_idx=idx, topk_w=p, **kw)
+    dx = blk.backward(torch.empty_like(e))
+    assert y.shape == h.shape == dx.shape == (0, d)
+    grads = dict(blk.layer.grads(), dw_norm=blk.dw_norm)
+    for name, v in grads.items():
+        assert not bool(v.any()), name

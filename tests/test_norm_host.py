@@ -147,3 +147,13 @@ def test_binding_refuses_row_counts_past_32_bits():
         L.moe_add_rmsnorm_bwd(x, x, w, torch.empty(T, device="meta"), x, dw=w)
     with pytest.raises(L.MoEError, match="rows"):
         L.moe_add_rmsnorm_bwd_workspace_bytes(T, 8)
+
+
+def test_norm_of_no_rows_needs_no_tensor():
+    """A tensor of no row may have no address."""
+    f = L.lib().moe_add_rmsnorm
+    for dtype in (0, 1):
+        assert f(dtype, None, None, FAKE, 0, 256, 1e-6, None, None, None, None, None, None) == 0
+        assert f(dtype, None, None, FAKE, 0, 12, 1e-6, None, None, None, None, None, None) == INVALID
+        assert f(dtype, None, None, FAKE, 0, 12296, 1e-6, None, None, None, None, None, None) == UNSUPPORTED
+    assert f(1, None, FAKE, FAKE, 4, 256, 1e-6, None, FAKE, None, None, None, None) == INVALID
