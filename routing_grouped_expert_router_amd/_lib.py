@@ -610,7 +610,7 @@ def moe_experts_w4(x, topk_idx, topk_w, w_gate: W4Tensor, w_up: W4Tensor, w_down
               *w_up._addresses("w_up", (E, d, F)), *w_down._addresses("w_down", (E, F, d)),
               _req(y_add, "y_add", bf, (T, d), optional=True), _req(y, "y", bf, (T, d)), _p(ws))
     try:
-        desc = moe_w4_desc(T, d, E, k, F, *fields, _nbytes(ws))
+        desc = moe_w4_desc(T, d, E, k, F, *fields, 0 if ws is None else _nbytes(ws))
     except TypeError:   # the stand-in for a host tensor is no address
         if any(f is _HOST for f in fields):
             raise MoEError("moe_experts_w4: libmoe needs device tensors") from None

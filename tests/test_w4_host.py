@@ -132,3 +132,12 @@ def test_decoder_hands_the_norm_no_rows_that_it_overwrites(rows, swap, monkeypat
     size = h.numel() * h.element_size()
     for t in (gx, gres):
         assert t.data_ptr() == h.data_ptr() or abs(t.data_ptr() - h.data_ptr()) >= size
+
+
+def test_missing_workspace_is_the_librarys_error():
+    T, d, E, k, F = 3, 256, 4, 2, 128
+    bf = torch.bfloat16
+    x, idx, p = torch.zeros(T, d, dtype=bf), torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k)
+    wg, wd = L.W4Tensor.empty(E, d, F, device="cpu"), L.W4Tensor.empty(E, F, d, device="cpu")
+    with pytest.raises(L.MoEError):
+        L.moe_experts_w4(x, idx, p, wg, wg, wd, x.clone(), None)
