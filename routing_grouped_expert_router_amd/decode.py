@@ -38,6 +38,8 @@ class MoEDecoder:
         E, d, F = w_gate.shape
         if max_tokens < 1 or max_tokens * k > L.MOE_W4_MAX_SLOTS:
             raise ValueError(f"1 <= max_tokens * k <= {L.MOE_W4_MAX_SLOTS}")
+        if not (w_gate_s is None) == (w_up_s is None) == (w_down_s is None):
+            raise ValueError("a shared expert needs all three of its weights")
         self.w_norm, self.w_r, self.k, self.eps = w_norm, w_r, k, eps
         self.T, self.d, self.E, self.F, self.dev = max_tokens, d, E, F, w_gate.device
         self.w4 = [quantize_experts(w) for w in (w_gate, w_up, w_down)]

@@ -141,3 +141,15 @@ def test_missing_workspace_is_the_librarys_error():
     wg, wd = L.W4Tensor.empty(E, d, F, device="cpu"), L.W4Tensor.empty(E, F, d, device="cpu")
     with pytest.raises(L.MoEError):
         L.moe_experts_w4(x, idx, p, wg, wg, wd, x.clone(), None)
+
+
+@pytest.mark.parametrize("given", [("w_gate_s",), ("w_up_s", "w_down_s"), ("w_down_s",)], ids=str)
+def test_decoder_refuses_part_of_a_shared_expert(given, monkeypatch):
+    monkeypatch.setattr(L, "moe_w4_quantize", lambda w, out: None)
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    shared = dict(w_gate_s=b(128, 128), w_up_s=b(128, 128), w_down_s=b(128, 128))
+    args = (b(128), b(128, 4), b(4, 128, 128), b(4, 128, 128), b(4, 128, 128))
+    with pytest.raises(ValueError, match="shared expert"):
+        MoEDecoder(*args, k=2, max_tokens=5, **{n: shared[n] for n in given})
+    assert MoEDecoder(*args, k=2, max_tokens=5, **shared).shared is not None
+    assert MoEDecoder(*args, k=2, max_tokens=5).shared is None
