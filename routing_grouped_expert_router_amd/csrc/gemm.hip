@@ -260,6 +260,9 @@ template <class C> int launch_ckpt_tiles(const moe_gg_desc* g, const GGArgs& a, 
 // rows, d 512, F 512, 16 experts (192 workgroups): 3.7 us less, 4096 rows, d 1024
 // (320): 8.6 more; data gradient, 4096 rows, d 1024, F 512, 16 experts (160): 11
 // less, 8192 rows (288): 2.0 more.
+// swz_k is chosen for rows of four chunks; these of eight keep it, at 0.22
+// (gate/up) and 0.40 bank conflicts an LDS access where the 128-row tiles have
+// 0.04 and 0.10.
 using CfgDmaSmall = DmaCfg<64, 256, 2, 4, 64, 3, 1>;
 int launch_ckpt(const moe_gg_desc* g, const GGArgs& a, int tiles_n, hipStream_t stream) {
   if (ckpt_grid<CfgDmaSmall>(g, tiles_n) <= 256) return launch_ckpt_tiles<WithCkpt<CfgDmaSmall>>(g, a, tiles_n, stream);
